@@ -16,7 +16,10 @@ import numpy as np
 from . import _lib as C
 from ._lib import MoeError  # noqa: F401
 
-__all__ = ["MoELayer", "Routing", "MoeError", "to_device", "bf16_tensor", "lib_path"]
+from .block import ACTS, AdamW, BlockNorm, GatedFFN, NormForward, NormGrads  # noqa: F401
+
+__all__ = ["MoELayer", "Routing", "MoeError", "to_device", "bf16_tensor", "lib_path", "GatedFFN", "BlockNorm", "AdamW",
+           "NormForward", "NormGrads", "ACTS"]
 
 
 def lib_path() -> str:

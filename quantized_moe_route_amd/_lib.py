@@ -26,7 +26,17 @@ EXPORTED = (
     "moe_backward_input", "moe_destroy", "moe_status_string", "moe_last_error",
     "moe_set_lora", "moe_backward_lora", "moe_check_status", "moe_forward_static",
     "moe_project_in", "moe_project_out", "moe_project_out_backward", "moe_project_in_backward", "moe_prof_enable", "moe_prof_read", "moe_prof_hbm_read",
+    "moe_ffn_desc_init", "moe_ffn_workspace_size", "moe_ffn_create", "moe_ffn_forward", "moe_ffn_backward", "moe_ffn_destroy",
+    "moe_norm_desc_init", "moe_norm_workspace_size", "moe_norm_create", "moe_norm_forward", "moe_norm_backward",
+    "moe_norm_destroy", "moe_adamw_desc_init", "moe_adamw_workspace_size", "moe_adamw_create", "moe_adamw_bind",
+    "moe_adamw_set_step", "moe_adamw_step", "moe_adamw_destroy",
 )
+
+# include/moe_block.h
+MOE_FFN_BACKWARD = 1
+MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN, MOE_GATE_FULL = range(4)
+MOE_NORM_POST, MOE_NORM_NEXT, MOE_NORM_BACKWARD = 1, 2, 4
+MOE_STATE_F32, MOE_STATE_E4M3 = 0, 1
 
 # kernel families of include/moe_prof.h
 PROF_ROUTER_LOGITS, PROF_ROUTER_TOPK, PROF_GROUP, PROF_GATEUP, PROF_DOWN, PROF_COMBINE, PROF_BWD_DOWN, \
@@ -58,6 +68,28 @@ class MoeLora(ctypes.Structure):
 
 class MoeRouting(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("ids", "w", "counts", "offsets", "perm", "inv", "active", "n_active")]
+
+
+class MoeFfnDesc(ctypes.Structure):
+    _fields_ = [("width", ctypes.c_int32), ("inter", ctypes.c_int32), ("max_tokens", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
+class MoeNormDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("width", "max_tokens", "r_dtype", "y_dtype", "x_dtype", "w_dtype", "gate")] + \
+               [(n, ctypes.c_float) for n in ("eps_post", "eps_next", "res_scale", "branch_scale")] + \
+               [("flags", ctypes.c_uint32)]
+
+
+class MoeAdamwDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_double) for n in ("beta1", "beta2", "eps", "max_norm")] + \
+               [("state", ctypes.c_int32), ("max_tensors", ctypes.c_int32), ("max_elements", ctypes.c_int64)]
+
+
+class MoeAdamwTensor(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("param", "master", "grad", "m", "v", "m_scale", "v_scale")] + \
+               [("n", ctypes.c_int64), ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
+                ("weight_decay", ctypes.c_float), ("lr_scale", ctypes.c_float)]
 
 
 class MoeError(RuntimeError):
@@ -111,6 +143,31 @@ def lib() -> ctypes.CDLL:
         L.moe_status_string.restype = ctypes.c_char_p
         L.moe_last_error.argtypes = []
         L.moe_last_error.restype = ctypes.c_char_p
+        size, ref = ctypes.POINTER(ctypes.c_size_t), ctypes.POINTER
+        dbl, i64 = ctypes.c_double, ctypes.c_int64
+        for fn, args in {
+            "moe_ffn_workspace_size": [ref(MoeFfnDesc), size],
+            "moe_ffn_create": [ref(MoeFfnDesc), vp, vp, vp, vp, ctypes.c_size_t, ref(vp)],
+            "moe_ffn_forward": [vp, vp, i32, vp, i32, i32, vp, vp],
+            "moe_ffn_backward": [vp, vp, vp, i32, vp, vp, i32, i32, vp, vp, vp, i32, vp],
+            "moe_norm_workspace_size": [ref(MoeNormDesc), size],
+            "moe_norm_create": [ref(MoeNormDesc), vp, vp, vp, ctypes.c_size_t, ref(vp)],
+            "moe_norm_forward": [vp, vp, vp, vp, i32, vp, vp, vp, vp],
+            "moe_norm_backward": [vp, vp, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp],
+            "moe_adamw_workspace_size": [ref(MoeAdamwDesc), size],
+            "moe_adamw_create": [ref(MoeAdamwDesc), vp, ctypes.c_size_t, ref(vp)],
+            "moe_adamw_bind": [vp, ref(MoeAdamwTensor), i32, vp],
+            "moe_adamw_set_step": [vp, i64, vp],
+            "moe_adamw_step": [vp, dbl, vp, vp, vp],
+        }.items():
+            getattr(L, fn).argtypes = args
+            getattr(L, fn).restype = st
+        for fn, desc in (("moe_ffn_desc_init", MoeFfnDesc), ("moe_norm_desc_init", MoeNormDesc), ("moe_adamw_desc_init", MoeAdamwDesc)):
+            getattr(L, fn).argtypes = [ref(desc)]
+            getattr(L, fn).restype = None
+        for fn in ("moe_ffn_destroy", "moe_norm_destroy", "moe_adamw_destroy"):
+            getattr(L, fn).argtypes = [vp]
+            getattr(L, fn).restype = None
         L.moe_prof_enable.argtypes = [vp, ctypes.c_uint32, i32]
         L.moe_prof_enable.restype = st
         L.moe_prof_read.argtypes = [vp, i32, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(i32)]

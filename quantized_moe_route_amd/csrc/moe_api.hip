@@ -15,6 +15,7 @@
 #include <new>
 #include <string>
 
+#include "api_status.h"
 #include "moe.h"
 #include "moe_internal.h"
 #include "moe_prof.h"
@@ -33,6 +34,28 @@ moe_status fail(moe_status s, const char *fmt, ...)
     g_last_error = buf;
     return s;
 }
+
+}  // namespace
+
+namespace moe {
+
+// the same for the other files of the C ABI (api_status.h)
+moe_status api_fail(moe_status s, const char *fmt, ...)
+{
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    g_last_error = buf;
+    return s;
+}
+
+void api_clear() { g_last_error.clear(); }
+
+}  // namespace moe
+
+namespace {
 
 constexpr int kMaxExperts = 2048;
 constexpr int kMaxTopK = 64;
