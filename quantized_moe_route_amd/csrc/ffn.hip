@@ -79,7 +79,8 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b)
 // KM = false: stored [row][k], LDS [row][64] with the 16-byte chunk c of row r at c ^ (r / 2 % 8).
 // KM = true: stored [k][row], LDS [k][ROWS] with chunk c of k at c ^ (4 (k % 4)) (64 rows: 4 (k % 2)):
 //   the four k of a transposing read's 16 lanes fall into four 64-byte groups.
-template <int ROWS, bool KM, int NW>
+// SPAN: the rows of one matrix that the tile covers (half of it where it holds two).
+template <int ROWS, bool KM, int NW, int kSpan = ROWS>
 struct Tile {
     static constexpr int kSwz = (ROWS / 8 - 1) & 12;
     static constexpr int kInstr = ROWS * kBK * 2 / 1024 / NW;  // 1 KB loads per wave
@@ -110,33 +111,31 @@ struct Tile {
         }
     }
 
-    // Base: the tile's first row at k = 0 of the segment.  rows_left rows (KM: columns) are valid.
-    __device__ __forceinline__ void load(uint16_t *lds, const uint16_t *base, int k0, int K, int wv, int lane) const
+    // Base: the tile's first row at k = 0 of the segment.  rows_left rows (KM: columns) are valid; live =
+    // false loads zeros only.  Row offsets of !KM tiles are in voff (the gate/up tile sets its own).
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t window(const uint16_t *base, int k0, int K, bool live) const
     {
+        uint32_t bytes;
         if constexpr (!KM) {
-            const uint32_t bytes = (uint32_t)(min(rows_left, ROWS) - 1) * ld * 2 + (uint32_t)(K - k0) * 2;
-            const auto r = rsrc_of(base + k0, bytes);
-            const bool tail = k0 + kBK > K;
-#pragma unroll
-            for (int i = 0; i < kInstr; i++) {
-                uint32_t v = voff[i];
-                if (tail) {
-                    const int row = 8 * (wv * kInstr + i) + (lane >> 3);
-                    const int c = (lane & 7) ^ ((row >> 1) & 7);
-                    if (k0 + 8 * c >= K) v = kOob;
-                }
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                    r, (__attribute__((address_space(3))) void *)(lds + 512 * (wv * kInstr + i)), 16, (int)v, 0, 0, 0);
-            }
+            bytes = (uint32_t)(min(rows_left, kSpan) - 1) * ld * 2 + (uint32_t)(K - k0) * 2;
+            base += k0;
         } else {
-            const int krows = min(kBK, K - k0);
-            const uint32_t bytes = (uint32_t)(krows - 1) * ld * 2 + (uint32_t)rows_left * 2;
-            const auto r = rsrc_of(base + (size_t)k0 * ld, bytes);
-#pragma unroll
-            for (int i = 0; i < kInstr; i++)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                    r, (__attribute__((address_space(3))) void *)(lds + 512 * (wv * kInstr + i)), 16, (int)voff[i], 0, 0, 0);
+            bytes = (uint32_t)(min(kBK, K - k0) - 1) * ld * 2 + (uint32_t)rows_left * 2;
+            base += (size_t)k0 * ld;
         }
+        return rsrc_of(base, live ? bytes : 0u);
+    }
+
+    // Piece i of the wave; pieces past the reduction's end (a whole number of 16-byte chunks) read zero.
+    __device__ __forceinline__ void piece(__amdgpu_buffer_rsrc_t r, uint16_t *lds, int i, int k0, int K, int wv, int lane) const
+    {
+        uint32_t v = voff[i];
+        if constexpr (!KM) {
+            const int row = 8 * (wv * kInstr + i) + (lane >> 3), c = (lane & 7) ^ ((row >> 1) & 7);
+            v = k0 + 8 * c < K ? v : kOob;
+        }
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)(lds + 512 * (wv * kInstr + i)), 16,
+                                                 (int)v, 0, 0, 0);
     }
 
     // Fragment of rows row0..row0+31, reduction 16 s..16 s + 15: lane l holds row l % 32, the
@@ -159,22 +158,131 @@ struct Tile {
     }
 };
 
-// Four consecutive values as `planes` bf16 rows, plane p at dst + p * stride: one rounding, or the
+// Eight consecutive values as `planes` bf16 rows, plane p at dst + p * stride: one rounding, or the
 // three terms whose sum is the value (a value that is not finite stays in the first term).
-__device__ __forceinline__ void put_planes(uint16_t *dst, size_t stride, int planes, const float (&f)[4])
+__device__ __forceinline__ void put_planes(uint16_t *dst, size_t stride, int planes, const float (&f)[8])
 {
-    *(u32x2 *)dst = u32x2{bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3])};
+    *(u32x4 *)dst = u32x4{bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7])};
     if (planes == 1) return;
-    float m[4], l[4];
+    float m[8], l[8];
 #pragma unroll
-    for (int e = 0; e < 4; e++) {
+    for (int e = 0; e < 8; e++) {
         const float hi = (float)(__bf16)f[e];
         const bool fin = fabsf(hi) < INFINITY;
         m[e] = fin ? f[e] - hi : 0.f;
         l[e] = m[e] - (float)(__bf16)m[e];
     }
-    *(u32x2 *)(dst + stride) = u32x2{bf16_pair(m[0], m[1]), bf16_pair(m[2], m[3])};
-    *(u32x2 *)(dst + 2 * stride) = u32x2{bf16_pair(l[0], l[1]), bf16_pair(l[2], l[3])};
+    *(u32x4 *)(dst + stride) = u32x4{bf16_pair(m[0], m[1]), bf16_pair(m[2], m[3]), bf16_pair(m[4], m[5]), bf16_pair(m[6], m[7])};
+    *(u32x4 *)(dst + 2 * stride) = u32x4{bf16_pair(l[0], l[1]), bf16_pair(l[2], l[3]), bf16_pair(l[4], l[5]), bf16_pair(l[6], l[7])};
+}
+
+__device__ __forceinline__ void put8(float *p, const float (&f)[8])
+{
+    *(f32x4 *)p = f32x4{f[0], f[1], f[2], f[3]};
+    *(f32x4 *)(p + 4) = f32x4{f[4], f[5], f[6], f[7]};
+}
+
+// Row r, columns 8 c .. 8 c + 7 of a wave's epilogue scratch.
+__device__ __forceinline__ void get8(const f32x4 *sc, int r, int c, float (&f)[8])
+{
+    const f32x4 a = sc[16 * r + ((2 * c) ^ (r & 15))], b = sc[16 * r + ((2 * c + 1) ^ (r & 15))];
+#pragma unroll
+    for (int e = 0; e < 4; e++) f[e] = a[e], f[4 + e] = b[e];
+}
+
+// Keeps a wave's writes to its own LDS ahead of its other lanes' reads (and the reverse).
+__device__ __forceinline__ void wave_fence()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// Scheduling hint for the instructions since the last one: the READS LDS reads spread over the MULS
+// matrix instructions.
+template <int READS, int MULS, int I = 0>
+__device__ __forceinline__ void interleave()
+{
+    constexpr int n = READS < MULS ? READS : MULS;
+    if constexpr (I < n) {
+        __builtin_amdgcn_sched_group_barrier(0x008, (I + 1) * MULS / n - I * MULS / n, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, (I + 1) * READS / n - I * READS / n, 0);
+        interleave<READS, MULS, I + 1>();
+    }
+}
+
+// The same with LOADS loads into LDS among them.
+template <int READS, int LOADS, int MULS, int I = 0>
+__device__ __forceinline__ void interleave_loads()
+{
+    if constexpr (I < MULS) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        if constexpr ((I + 1) * LOADS / MULS - I * LOADS / MULS > 0)
+            __builtin_amdgcn_sched_group_barrier(0x020, (I + 1) * LOADS / MULS - I * LOADS / MULS, 0);
+        if constexpr ((I + 1) * READS / MULS - I * READS / MULS > 0)
+            __builtin_amdgcn_sched_group_barrier(0x100, (I + 1) * READS / MULS - I * READS / MULS, 0);
+        interleave_loads<READS, LOADS, MULS, I + 1>();
+    }
+}
+
+// What becomes of eight consecutive values of a product (u: the up values beside gate values v).
+template <int EPI>
+__device__ __forceinline__ void epilogue(const GemmArgs &g, int z, int m, int n, float (&v)[8], const float (&u)[8])
+{
+    if constexpr (EPI == EPI_STORE) {
+        const size_t at = (size_t)m * g.N + n;
+        if (g.ct == DT_F32) {
+            float *p = (float *)g.c[z] + at;
+            if (g.acc) {
+                const f32x4 a = *(const f32x4 *)p, b = *(const f32x4 *)(p + 4);
+#pragma unroll
+                for (int e = 0; e < 4; e++) v[e] += a[e], v[4 + e] += b[e];
+            }
+            put8(p, v);
+        } else {
+            uint16_t *p = (uint16_t *)g.c[z] + at;
+            if (g.acc) {
+                const u32x4 b = *(const u32x4 *)p;
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    v[2 * e] += __uint_as_float(b[e] << 16);
+                    v[2 * e + 1] += __uint_as_float(b[e] & 0xFFFF0000u);
+                }
+            }
+            put_planes(p, 0, 1, v);
+        }
+    } else if constexpr (EPI == EPI_GU) {
+        if (g.h) {
+            float h[8];
+#pragma unroll
+            for (int e = 0; e < 8; e++) h[e] = act_h(g.act, v[e], u[e]);
+            put_planes(g.h + (size_t)m * g.N + n, (size_t)g.M * g.N, g.planes, h);
+        }
+        if (g.gu) {
+            float *p = g.gu + (size_t)m * 2 * g.N + n;
+            put8(p, v);
+            put8(p + g.N, u);
+        }
+    } else {
+        const float *p = g.gu + (size_t)m * 2 * g.N + n;
+        float h[8], dg[8], du[8];
+#pragma unroll
+        for (int q = 0; q < 2; q++) {
+            const f32x4 gv = *(const f32x4 *)(p + 4 * q), uv = *(const f32x4 *)(p + g.N + 4 * q);
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const int k = 4 * q + e;
+                act_grad(g.act, gv[e], uv[e], h[k], dg[k], du[k]);
+                dg[k] *= v[k];
+                du[k] *= v[k];
+            }
+        }
+        if (g.h) put_planes(g.h + (size_t)m * g.N + n, (size_t)g.M * g.N, g.planes, h);
+        if (g.dgu) {
+            uint16_t *o = g.dgu + (size_t)m * 2 * g.N + n;
+            put_planes(o, (size_t)g.M * 2 * g.N, g.planes, dg);
+            put_planes(o + g.N, (size_t)g.M * 2 * g.N, g.planes, du);
+        }
+    }
 }
 
 // Tile of the block's index: each XCD (blocks b % 8) takes a run of tiles, walked in groups of
@@ -193,7 +301,7 @@ __device__ __forceinline__ void tile_of(int nm, int nn, int &tm, int &tn)
 // WM x WN waves.  EPI_GU: the B tile holds groups of 32 rows, alternately of the gate and the up
 // matrix, so a wave's column tiles 2 j and 2 j + 1 are gate and up of the same columns.
 template <int BM, int BN, int WM, int WN, bool AK, bool BKM, int EPI>
-__global__ __launch_bounds__(64 * WM *WN) void k_ffn_gemm(GemmArgs g)
+__global__ __launch_bounds__(64 * WM *WN, 1) void k_ffn_gemm(GemmArgs g)
 {
     constexpr int NW = WM * WN, TM = BM / WM / 32, TN = BN / WN / 32;
     constexpr bool GU = EPI == EPI_GU;
@@ -207,7 +315,7 @@ __global__ __launch_bounds__(64 * WM *WN) void k_ffn_gemm(GemmArgs g)
     const int m0 = tm * BM, n0 = tn * BNC, z = blockIdx.y;
 
     Tile<BM, AK, NW> ta;
-    Tile<BN, BKM, NW> tb;
+    Tile<BN, BKM, NW, BNC> tb;
     ta.init(wv, lane, g.M - m0, g.lda);
     tb.init(wv, lane, g.N - n0, g.ldb);
     if constexpr (GU) {
@@ -230,134 +338,120 @@ __global__ __launch_bounds__(64 * WM *WN) void k_ffn_gemm(GemmArgs g)
 
     const int ksteps = (g.K + kBK - 1) / kBK, nsteps = ksteps * g.nseg;
     int lseg = 0, lk = 0;  // segment and k of the next load
+    // The next tile into as, bs; after the last one zeros, so that the loop needs no branch.
     auto load = [&](uint16_t *as, uint16_t *bs) {
-        const Seg s = g.seg[z][lseg];
-        ta.load(as, AK ? s.a + m0 : s.a + (size_t)m0 * g.lda, lk, g.K, wv, lane);
-        if constexpr (GU) {
-            const uint32_t bytes = (uint32_t)(min(g.N - n0, BNC) - 1) * g.ldb * 2 + (uint32_t)(g.K - lk) * 2;
-            const auto rg = rsrc_of(s.b + (size_t)n0 * g.ldb + lk, bytes), ru = rsrc_of(g.b2 + (size_t)n0 * g.ldb + lk, bytes);
-            const bool tail = lk + kBK > g.K;
+        const bool live = lseg < g.nseg;
+        const Seg s = g.seg[z][live ? lseg : 0];
+        const auto ra = ta.window(AK ? s.a + m0 : s.a + (size_t)m0 * g.lda, lk, g.K, live);
+        const auto rb = tb.window(BKM ? s.b + n0 : s.b + (size_t)n0 * g.ldb, lk, g.K, live);
 #pragma unroll
-            for (int i = 0; i < tb.kInstr; i++) {
-                const int piece = wv * tb.kInstr + i;  // 8 rows, all of one matrix
-                uint32_t v = tb.voff[i];
-                if (tail) {
-                    const int r = 8 * piece + (lane >> 3);
-                    if (lk + 8 * ((lane & 7) ^ ((r >> 1) & 7)) >= g.K) v = kOob;
-                }
-                auto *dst = (__attribute__((address_space(3))) void *)(bs + 512 * piece);
-                if ((piece >> 2) & 1)
-                    __builtin_amdgcn_raw_ptr_buffer_load_lds(ru, dst, 16, (int)v, 0, 0, 0);
-                else
-                    __builtin_amdgcn_raw_ptr_buffer_load_lds(rg, dst, 16, (int)v, 0, 0, 0);
-            }
+        for (int i = 0; i < ta.kInstr; i++) ta.piece(ra, as, i, lk, g.K, wv, lane);
+        if constexpr (GU) {
+            const auto ru = tb.window(g.b2 + (size_t)n0 * g.ldb, lk, g.K, live);
+#pragma unroll
+            for (int i = 0; i < tb.kInstr; i++)  // eight rows, all of one matrix
+                tb.piece(((wv * tb.kInstr + i) >> 2) & 1 ? ru : rb, bs, i, lk, g.K, wv, lane);
         } else {
-            tb.load(bs, BKM ? s.b + n0 : s.b + (size_t)n0 * g.ldb, lk, g.K, wv, lane);
+#pragma unroll
+            for (int i = 0; i < tb.kInstr; i++) tb.piece(rb, bs, i, lk, g.K, wv, lane);
         }
         lk += kBK;
-        if (lk >= g.K) {
-            lk = 0;
-            lseg++;
-        }
+        const bool over = lk >= g.K;
+        lk = over ? 0 : lk;
+        lseg += over;
     };
-    auto mul = [&](const uint16_t *as, const uint16_t *bs) {
+    // Fragments of the 16 reduction indices s of a tile.
+    bf16x8 fa[2][TM], fb[2][TN];
+    auto read = [&](auto P, const uint16_t *as, const uint16_t *bs, int s) {
+        constexpr int p = decltype(P)::value;
 #pragma unroll
-        for (int s = 0; s < kBK / 16; s++) {
-            bf16x8 fa[TM], fb[TN];
+        for (int j = 0; j < TN; j++) fb[p][j] = Tile<BN, BKM, NW>::frag(bs, 32 * (wn * TN + j), s, lane);
 #pragma unroll
-            for (int i = 0; i < TM; i++) fa[i] = Tile<BM, AK, NW>::frag(as, 32 * (wm * TM + i), s, lane);
+        for (int i = 0; i < TM; i++) fa[p][i] = Tile<BM, AK, NW>::frag(as, 32 * (wm * TM + i), s, lane);
+    };
+    // the B rows (output columns) take the MFMA's row side: a lane ends up with columns
+    // 8 q + 4 (lane / 32) + 0..3 of row lane % 32
+    auto mul = [&](auto P) {
+        constexpr int p = decltype(P)::value;
 #pragma unroll
-            for (int j = 0; j < TN; j++) fb[j] = Tile<BN, BKM, NW>::frag(bs, 32 * (wn * TN + j), s, lane);
-            // the B rows (output columns) take the MFMA's row side: a lane ends up with
-            // columns 8 q + 4 (lane / 32) + 0..3 of row lane % 32
+        for (int i = 0; i < TM; i++)
 #pragma unroll
-            for (int i = 0; i < TM; i++)
-#pragma unroll
-                for (int j = 0; j < TN; j++) acc[i][j] = mfma32(fb[j], fa[i], acc[i][j]);
-        }
+            for (int j = 0; j < TN; j++) acc[i][j] = mfma32(fb[p][j], fa[p][i], acc[i][j]);
+    };
+    using E = std::integral_constant<int, 0>;
+    using O = std::integral_constant<int, 1>;
+    constexpr int kReads = TN * (BKM ? 2 : 1) + TM * (AK ? 2 : 1), kMul = TM * TN;
+    // One tile of 64 k: the fragments of the next 16 k are read while the present ones are multiplied.
+    // One barrier a tile, before its last 16 k: by then every wave has read all of this buffer (so the
+    // tile after next may stream into it) and has seen its own part of the next tile arrive.
+    auto step = [&](const uint16_t *as, const uint16_t *bs, uint16_t *lda_, uint16_t *ldb_, const uint16_t *an, const uint16_t *bn) {
+        read(O(), as, bs, 1);
+        mul(E());
+        interleave<kReads, kMul>();
+        read(E(), as, bs, 2);
+        mul(O());
+        interleave<kReads, kMul>();
+        read(O(), as, bs, 3);
+        mul(E());
+        interleave<kReads, kMul>();
+        wait_vm<0>();
+        __syncthreads();
+        load(lda_, ldb_);
+        read(E(), an, bn, 0);  // past the last tile: zeros, not used
+        mul(O());
+        interleave_loads<kReads, ta.kInstr + tb.kInstr, kMul>();
     };
 
     load(as0, bs0);
+    load(as1, bs1);
     wait_vm<0>();
     __syncthreads();
-    for (int st = 0; st < nsteps; st += 2) {
-        if (st + 1 < nsteps) load(as1, bs1);
-        mul(as0, bs0);
-        wait_vm<0>();
-        __syncthreads();
-        if (st + 1 < nsteps) {
-            if (st + 2 < nsteps) load(as0, bs0);
-            mul(as1, bs1);
-            wait_vm<0>();
-            __syncthreads();
-        }
+    read(E(), as0, bs0, 0);
+    int st = 0;
+    for (; st + 2 <= nsteps; st += 2) {
+        step(as0, bs0, as0, bs0, as1, bs1);
+        step(as1, bs1, as1, bs1, as0, bs0);
     }
+    if (st < nsteps) step(as0, bs0, as0, bs0, as1, bs1);
+    wait_vm<0>();  // the zeros behind the last tile have landed before the epilogue uses the buffers
+    __syncthreads();
 
-    const int cl = 4 * (lane >> 5);
+    // Epilogue: a wave's 32 x 64 part at a time goes through its own 8 KB of LDS (16-byte chunk c of a
+    // row at c ^ (row % 16)), so that a lane ends up with eight consecutive columns of a row and the
+    // stores cover whole lines; the loop over the rows stays rolled.
+    uint16_t *const pool[4] = {as0, as1, bs0, bs1};
+    constexpr int kPer = NW > 4 ? NW / 4 : 1;
+    static_assert(TN % 2 == 0 && kPer * 8192 <= BM * kBK * 2 && kPer * 8192 <= BN * kBK * 2, "epilogue scratch");
+    uint16_t *slot = as0;
 #pragma unroll
-    for (int i = 0; i < TM; i++) {
-        const int m = m0 + 32 * (wm * TM + i) + (lane & 31);
-        if (m >= g.M) continue;
+    for (int k = 1; k < 4; k++)
+        if (wv / kPer == k) slot = pool[k];
+    f32x4 *const sc = (f32x4 *)(slot + 4096 * (wv % kPer));
 #pragma unroll
-        for (int j = 0; j < TN; j += GU ? 2 : 1) {
-            const int nb = GU ? n0 + 16 * (wn * TN + j) : n0 + 32 * (wn * TN + j);
+    for (int i = 0; i < TM; i++)
 #pragma unroll
-            for (int q = 0; q < 4; q++) {
-                const int n = nb + 8 * q + cl;
-                if (n >= g.N) continue;
-                float v[4];
+        for (int j = 0; j < TN; j += 2) {
+            wave_fence();
 #pragma unroll
-                for (int e = 0; e < 4; e++) v[e] = acc[i][j][4 * q + e];
-                if constexpr (EPI == EPI_STORE) {
-                    const size_t at = (size_t)m * g.N + n;
-                    if (g.ct == DT_F32) {
-                        f32x4 *p = (f32x4 *)((float *)g.c[z] + at);
-                        f32x4 o = {v[0], v[1], v[2], v[3]};
-                        if (g.acc) o += *p;
-                        *p = o;
-                    } else {
-                        u32x2 *p = (u32x2 *)((uint16_t *)g.c[z] + at);
-                        if (g.acc) {
-                            const u32x2 b = *p;
-                            v[0] += __uint_as_float(b[0] << 16);
-                            v[1] += __uint_as_float(b[0] & 0xFFFF0000u);
-                            v[2] += __uint_as_float(b[1] << 16);
-                            v[3] += __uint_as_float(b[1] & 0xFFFF0000u);
-                        }
-                        *p = u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
-                    }
-                } else if constexpr (GU) {
-                    float u[4], h[4];
+            for (int d = 0; d < 2; d++)
 #pragma unroll
-                    for (int e = 0; e < 4; e++) u[e] = acc[i][(j + 1) % TN][4 * q + e];
-#pragma unroll
-                    for (int e = 0; e < 4; e++) h[e] = act_h(g.act, v[e], u[e]);
-                    if (g.h) put_planes(g.h + (size_t)m * g.N + n, (size_t)g.M * g.N, g.planes, h);
-                    if (g.gu) {
-                        float *p = g.gu + (size_t)m * 2 * g.N + n;
-                        *(f32x4 *)p = f32x4{v[0], v[1], v[2], v[3]};
-                        *(f32x4 *)(p + g.N) = f32x4{u[0], u[1], u[2], u[3]};
-                    }
-                } else {
-                    const float *p = g.gu + (size_t)m * 2 * g.N + n;
-                    const f32x4 gv = *(const f32x4 *)p, uv = *(const f32x4 *)(p + g.N);
-                    float h[4], dg[4], du[4];
-#pragma unroll
-                    for (int e = 0; e < 4; e++) {
-                        act_grad(g.act, gv[e], uv[e], h[e], dg[e], du[e]);
-                        dg[e] *= v[e];
-                        du[e] *= v[e];
-                    }
-                    if (g.h) put_planes(g.h + (size_t)m * g.N + n, (size_t)g.M * g.N, g.planes, h);
-                    if (g.dgu) {
-                        uint16_t *o = g.dgu + (size_t)m * 2 * g.N + n;
-                        put_planes(o, (size_t)g.M * 2 * g.N, g.planes, dg);
-                        put_planes(o + g.N, (size_t)g.M * 2 * g.N, g.planes, du);
-                    }
+                for (int q = 0; q < 4; q++) {
+                    const int m = lane & 31, c = 8 * d + 2 * q + (lane >> 5);
+                    sc[16 * m + (c ^ (m & 15))] = f32x4{acc[i][j + d][4 * q], acc[i][j + d][4 * q + 1], acc[i][j + d][4 * q + 2], acc[i][j + d][4 * q + 3]};
                 }
+            wave_fence();
+            const int mb = m0 + 32 * (wm * TM + i);
+            const int nb = GU ? n0 + 16 * (wn * TN + j) : n0 + 32 * (wn * TN + j);
+            constexpr int lpr = GU ? 4 : 8;  // lanes per row
+#pragma unroll 1
+            for (int r0 = 0; r0 < 32; r0 += 64 / lpr) {
+                const int r = r0 + lane / lpr, cb = lane % lpr, m = mb + r, n = nb + 8 * cb;
+                float v[8], u[8];
+                get8(sc, r, cb, v);
+                if constexpr (GU) get8(sc, r, 4 + cb, u);
+                if (m < g.M && n < g.N) epilogue<EPI>(g, z, m, n, v, u);
             }
         }
-    }
 }
 
 template <int BM, int BN, int WM, int WN, bool AK, bool BKM, int EPI>
@@ -374,7 +468,7 @@ hipError_t gemm(const GemmArgs &g, int nz, hipStream_t s)
 {
     constexpr int cols = EPI == EPI_GU ? 2 : 1;
     const size_t big = (size_t)((g.M + 255) / 256) * ((cols * (size_t)g.N + 255) / 256) * nz;
-    if (big >= 200) return go<256, 256, 2, 4, AK, BKM, EPI>(g, nz, s);
+    if (big >= 200) return go<256, 256, 2, 2, AK, BKM, EPI>(g, nz, s);
     const size_t mid = (size_t)((g.M + 127) / 128) * ((cols * (size_t)g.N + 127) / 128) * nz;
     if (mid >= 200) return go<128, 128, 2, 2, AK, BKM, EPI>(g, nz, s);
     return go<64, 64, 2, 1, AK, BKM, EPI>(g, nz, s);
