@@ -7,13 +7,15 @@
 //   d x       A = dg | du [T][2I],   B = Wg, Wu [I][D] by k epilogue: dx
 //   d W       A = dg, du or dy by k, B = x or h by k        epilogue: dW
 // "by k": stored [k][n], the reduction over rows.  One kernel template covers them: an operand
-// stored along k is staged in LDS as [row][64 k]; one stored by k as [64 k][row], read with the
+// stored along k is staged in LDS as [row][32 k]; one stored by k as [32 k][row], read with the
 // transposing LDS read.  A product may run over several (A, B) pairs in turn ("segments"): dg and
 // du, and the three bf16 terms of an operand carried exactly.
 //
-// A block owns a BM x BN tile of C; its waves own WM x WN parts of it as 32 x 32 MFMA tiles.
-// Both operands stream straight into LDS (16 bytes a lane) into one of two buffers while the
-// other is multiplied.
+// A block owns a BM x BN tile of C at a time; its waves own parts of it as 32 x 32 MFMA tiles.  Both
+// operands stream straight into LDS (16 bytes a lane) into a ring of four buffers of 32 k, three
+// steps ahead of the multiplication.  The blocks are persistent: each walks tiles b, b + gridDim, ..., and the stream of
+// loads runs on into the next tile while the present one's results are stored through LDS scratch of
+// their own, so the matrix pipes wait neither for a first load nor for the last store.
 #include <type_traits>
 
 #include "block_internal.h"
@@ -27,27 +29,31 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short v4i16 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
 
-constexpr int kBK = 64;       // reduction indices per step
+constexpr int kBK = 32;       // reduction indices per step
+constexpr int kBufs = 4;      // LDS buffers of a step each
 constexpr int kMaxSeg = 6;
 constexpr uint32_t kOob = 0x80000000u;  // an offset past every buffer: reads zero
 
 enum { EPI_STORE = 0, EPI_GU = 1, EPI_DGU = 2 };
 
-struct Seg {
-    const uint16_t *a, *b;
+// One product.
+struct Prob {
+    int M, N, lda, ldb;  // lda, ldb: elements between rows of A and B as stored
+    int tiles;           // number of output tiles (set by the launcher)
+    const uint16_t *a[kMaxSeg], *b[kMaxSeg];
+    void *c;             // EPI_STORE
 };
 
+// Up to three products with the same reduction, walked as one list of tiles.
 struct GemmArgs {
-    int M, N, K;          // K: reduction length of each segment
-    int lda, ldb;         // elements between rows of A and B as stored
-    int nseg;
-    Seg seg[2][kMaxSeg];  // [blockIdx.y]
+    Prob p[3];
+    int np, nseg, K;      // K: reduction length of each segment
+    int tiles;
     const uint16_t *b2;   // EPI_GU: the up matrix (b of the segment is the gate matrix)
-    void *c[2];           // EPI_STORE: [blockIdx.y]
-    int ct;
+    int ct;               // EPI_STORE: dtype of c
     bool acc;
     // EPI_GU, EPI_DGU
-    int act, planes;
+    int planes;
     uint16_t *h, *dgu;
     float *gu;            // EPI_GU: written unless null; EPI_DGU: read
 };
@@ -76,64 +82,68 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b)
 }
 
 // One operand's tile of ROWS rows (of the output side) by kBK: its loader and its MFMA fragments.
-// KM = false: stored [row][k], LDS [row][64] with the 16-byte chunk c of row r at c ^ (r / 2 % 8).
+// KM = false: stored [row][k], LDS [row][32] with the 16-byte chunk c of row r at c ^ (r / 4 % 4).
 // KM = true: stored [k][row], LDS [k][ROWS] with chunk c of k at c ^ (4 (k % 4)) (64 rows: 4 (k % 2)):
 //   the four k of a transposing read's 16 lanes fall into four 64-byte groups.
-// SPAN: the rows of one matrix that the tile covers (half of it where it holds two).
-template <int ROWS, bool KM, int NW, int kSpan = ROWS>
+// Either way no LDS access of a wave meets a bank twice.  SPAN: the rows of one matrix that the tile
+// covers (half of it where it holds two).
+template <int ROWS, bool KM, int NW, int SPAN = ROWS>
 struct Tile {
     static constexpr int kSwz = (ROWS / 8 - 1) & 12;
     static constexpr int kInstr = ROWS * kBK * 2 / 1024 / NW;  // 1 KB loads per wave
     static_assert(kInstr >= 1 && kInstr * NW * 1024 == ROWS * kBK * 2, "tile split over the waves");
-    uint32_t voff[kInstr];  // byte offset of this lane's piece, without the step's part
-    int kc;                 // !KM: first k of the lane's piece
-    int rows_left, ld;
+    static_assert(!KM || (ROWS / 8 & (ROWS / 8 - 1)) == 0 || ROWS % 128 == 64, "swizzle stays in the row");
+    int chunk[kInstr];      // first k (KM: row) of this lane's piece i
+    int line[kInstr];       // its row (KM: k)
+    uint32_t voff[kInstr];  // its byte offset in the present product's operand
 
-    __device__ __forceinline__ void init(int wv, int lane, int rows_left_, int ld_)
+    __device__ __forceinline__ void init(int wv, int lane)
     {
-        rows_left = rows_left_;
-        ld = ld_;
-        if constexpr (!KM) {
-            // piece i of wave wv: rows 8 (wv kInstr + i) .. + 7
 #pragma unroll
-            for (int i = 0; i < kInstr; i++) {
-                const int r = 8 * (wv * kInstr + i) + (lane >> 3);
-                const int c = (lane & 7) ^ ((r >> 1) & 7);
-                voff[i] = r < rows_left ? ((uint32_t)r * ld + 8 * c) * 2 : kOob;
-            }
-        } else {
-            constexpr int cpr = ROWS / 8;  // chunks per k
-#pragma unroll
-            for (int i = 0; i < kInstr; i++) {
-                const int s = 64 * (wv * kInstr + i) + lane, k = s / cpr, c = (s % cpr) ^ ((k << 2) & kSwz);
-                voff[i] = 8 * c < rows_left ? ((uint32_t)k * ld + 8 * c) * 2 : kOob;
+        for (int i = 0; i < kInstr; i++) {
+            if constexpr (!KM) {
+                line[i] = 16 * (wv * kInstr + i) + (lane >> 2);
+                chunk[i] = 8 * ((lane & 3) ^ ((line[i] >> 2) & 3));
+                if (SPAN < ROWS) line[i] = 32 * (line[i] >> 6) + (line[i] & 31);  // groups of 32 rows, alternately of two matrices
+            } else {
+                constexpr int cpr = ROWS / 8;  // chunks per k
+                const int s = 64 * (wv * kInstr + i) + lane;
+                line[i] = s / cpr;
+                chunk[i] = 8 * ((s % cpr) ^ ((line[i] << 2) & kSwz));
             }
         }
     }
 
-    // Base: the tile's first row at k = 0 of the segment.  rows_left rows (KM: columns) are valid; live =
-    // false loads zeros only.  Row offsets of !KM tiles are in voff (the gate/up tile sets its own).
-    __device__ __forceinline__ __amdgpu_buffer_rsrc_t window(const uint16_t *base, int k0, int K, bool live) const
+    // For the tile that the loads turn to: rows of ld elements, of which (KM) left are valid.
+    __device__ __forceinline__ void turn(int left, int ld)
+    {
+#pragma unroll
+        for (int i = 0; i < kInstr; i++) {
+            voff[i] = ((uint32_t)line[i] * (uint32_t)ld + (uint32_t)chunk[i]) * 2;
+            if (KM && chunk[i] >= left) voff[i] = kOob;
+        }
+    }
+
+    // The part of the operand that a step's pieces may read: base is the tile's first row at k = 0 of the
+    // segment, left rows (KM: columns) are valid from there on.  live = false: zeros only.
+    static __device__ __forceinline__ __amdgpu_buffer_rsrc_t window(const uint16_t *base, int left, int ld, int k0, int K, bool live)
     {
         uint32_t bytes;
         if constexpr (!KM) {
-            bytes = (uint32_t)(min(rows_left, kSpan) - 1) * ld * 2 + (uint32_t)(K - k0) * 2;
+            // a row past the last begins behind this many bytes, since K - k0 <= ld
+            bytes = (uint32_t)(min(left, SPAN) - 1) * ld * 2 + (uint32_t)(K - k0) * 2;
             base += k0;
         } else {
-            bytes = (uint32_t)(min(kBK, K - k0) - 1) * ld * 2 + (uint32_t)rows_left * 2;
+            bytes = (uint32_t)(min(kBK, K - k0) - 1) * ld * 2 + (uint32_t)left * 2;
             base += (size_t)k0 * ld;
         }
         return rsrc_of(base, live ? bytes : 0u);
     }
 
-    // Piece i of the wave; pieces past the reduction's end (a whole number of 16-byte chunks) read zero.
-    __device__ __forceinline__ void piece(__amdgpu_buffer_rsrc_t r, uint16_t *lds, int i, int k0, int K, int wv, int lane) const
+    // Piece i of the wave; of !KM those past the reduction's end (a whole number of 16-byte chunks) read zero.
+    __device__ __forceinline__ void piece(__amdgpu_buffer_rsrc_t r, uint16_t *lds, int i, int room, int wv) const
     {
-        uint32_t v = voff[i];
-        if constexpr (!KM) {
-            const int row = 8 * (wv * kInstr + i) + (lane >> 3), c = (lane & 7) ^ ((row >> 1) & 7);
-            v = k0 + 8 * c < K ? v : kOob;
-        }
+        const uint32_t v = KM || chunk[i] < room ? voff[i] : kOob;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)(lds + 512 * (wv * kInstr + i)), 16,
                                                  (int)v, 0, 0, 0);
     }
@@ -144,7 +154,7 @@ struct Tile {
     {
         if constexpr (!KM) {
             const int r = row0 + (lane & 31), c = 2 * s + (lane >> 5);
-            return as_bf16x8(*(const u32x4 *)(lds + r * kBK + 8 * (c ^ ((r >> 1) & 7))));
+            return as_bf16x8(*(const u32x4 *)(lds + r * kBK + 8 * (c ^ ((r >> 2) & 3))));
         } else {
             // 16-lane group q: rows 16 (q % 2), k from 8 (q / 2); lane i of it addresses k i / 4, rows 4 (i % 4)
             const int q = lane >> 4, i = lane & 15;
@@ -157,6 +167,53 @@ struct Tile {
         }
     }
 };
+
+// Reciprocal to 1 ulp (v_rcp_f32): the correctly rounded division takes ten instructions, and an
+// epilogue's exponentials and divisions stand between two tiles of matrix work.
+__device__ __forceinline__ float rcp(float z) { return __builtin_amdgcn_rcpf(z); }
+
+__device__ __forceinline__ float sigm(float z) { return rcp(1.f + __expf(-z)); }
+
+// tanh z = sign(z) (1 - e) / (1 + e), e = exp(-2 |z|); below 1/8, where 1 - e cancels, the odd series
+// to z^7 (its next term is below 2^-29 of z there).
+__device__ __forceinline__ float tanh_(float z)
+{
+    const float e = __expf(-2.f * fabsf(z)), z2 = z * z;
+    const float s = z * (1.f + z2 * (-1.f / 3.f + z2 * (2.f / 15.f + z2 * (-17.f / 315.f))));
+    return z2 < 1.f / 64.f ? s : copysignf((1.f - e) * rcp(1.f + e), z);
+}
+
+// The layer's activations (moe_act): h and its two derivatives.
+template <int ACT>
+__device__ __forceinline__ float gated(float g, float u)
+{
+    if constexpr (ACT == ACT_SITU) return 4.f * tanh_(0.25f * g) * sigm(g) * (25.f * tanh_(u * (1.f / 25.f)));
+    return g * sigm(g) * u;
+}
+
+__device__ __forceinline__ float sech2(float z)
+{
+    const float e = __expf(-2.f * fabsf(z)), r = rcp(1.f + e);
+    return 4.f * e * r * r;
+}
+
+template <int ACT>
+__device__ __forceinline__ void gated_grad(float g, float u, float &h, float &dhdg, float &dhdu)
+{
+    const float s = sigm(g);
+    if constexpr (ACT == ACT_SITU) {
+        const float zg = 0.25f * g, zu = u * (1.f / 25.f);
+        const float A = 4.f * tanh_(zg) * s, B = 25.f * tanh_(zu);
+        h = A * B;
+        dhdg = (sech2(zg) * s + A * (1.f - s)) * B;
+        dhdu = A * sech2(zu);
+        return;
+    }
+    const float silu = g * s;
+    h = silu * u;
+    dhdg = u * (s + silu * (1.f - s));
+    dhdu = silu;
+}
 
 // Eight consecutive values as `planes` bf16 rows, plane p at dst + p * stride: one rounding, or the
 // three terms whose sum is the value (a value that is not finite stays in the first term).
@@ -182,12 +239,32 @@ __device__ __forceinline__ void put8(float *p, const float (&f)[8])
     *(f32x4 *)(p + 4) = f32x4{f[4], f[5], f[6], f[7]};
 }
 
-// Row r, columns 8 c .. 8 c + 7 of a wave's epilogue scratch.
+// A wave's epilogue scratch: one 32 x 32 MFMA tile in fp32, 16-byte chunk c of row r at c ^ (r % 8).
+// put_tile takes the accumulator's layout (columns 8 q + 4 (lane / 32) + 0..3 of row lane % 32), get8 a
+// row's eight consecutive columns 8 c .. 8 c + 7.
+template <typename F>
+__device__ __forceinline__ void put_tile(f32x4 *sc, int lane, F &&value)
+{
+    const int m = lane & 31;
+#pragma unroll
+    for (int q = 0; q < 4; q++) sc[8 * m + ((2 * q + (lane >> 5)) ^ (m & 7))] = f32x4{value(4 * q), value(4 * q + 1), value(4 * q + 2), value(4 * q + 3)};
+}
+
 __device__ __forceinline__ void get8(const f32x4 *sc, int r, int c, float (&f)[8])
 {
-    const f32x4 a = sc[16 * r + ((2 * c) ^ (r & 15))], b = sc[16 * r + ((2 * c + 1) ^ (r & 15))];
+    const f32x4 a = sc[8 * r + ((2 * c) ^ (r & 7))], b = sc[8 * r + ((2 * c + 1) ^ (r & 7))];
 #pragma unroll
     for (int e = 0; e < 4; e++) f[e] = a[e], f[4 + e] = b[e];
+}
+
+// f(0), f(1), ... with compile-time numbers, so that what they index stays in registers.
+template <int N, typename F, int I = 0>
+__device__ __forceinline__ void each(F &&f)
+{
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>());
+        each<N, F, I + 1>(static_cast<F &&>(f));
+    }
 }
 
 // Keeps a wave's writes to its own LDS ahead of its other lanes' reads (and the reverse).
@@ -195,177 +272,157 @@ __device__ __forceinline__ void wave_fence()
 {
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_sched_barrier(0);  // and one tile's registers out of the next tile's way
 }
 
-// Scheduling hint for the instructions since the last one: the READS LDS reads spread over the MULS
-// matrix instructions.
-template <int READS, int MULS, int I = 0>
+// Scheduling hint for the instructions since the last one: an LDS read after each of the first matrix
+// instructions, so that the last read has half of them to come back in, and the LOADS loads into LDS
+// spread evenly.
+template <int READS, int LOADS, int MULS, int I = 0>
 __device__ __forceinline__ void interleave()
 {
-    constexpr int n = READS < MULS ? READS : MULS;
-    if constexpr (I < n) {
-        __builtin_amdgcn_sched_group_barrier(0x008, (I + 1) * MULS / n - I * MULS / n, 0);
-        __builtin_amdgcn_sched_group_barrier(0x100, (I + 1) * READS / n - I * READS / n, 0);
-        interleave<READS, MULS, I + 1>();
-    }
-}
-
-// The same with LOADS loads into LDS among them.
-template <int READS, int LOADS, int MULS, int I = 0>
-__device__ __forceinline__ void interleave_loads()
-{
     if constexpr (I < MULS) {
+        constexpr int per = (READS + MULS / 2 - 1) / (MULS / 2);  // reads a matrix instruction
+        constexpr int reads = I * per < READS ? (READS - I * per < per ? READS - I * per : per) : 0;
+        constexpr int loads = (I + 1) * LOADS / MULS - I * LOADS / MULS;
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        if constexpr ((I + 1) * LOADS / MULS - I * LOADS / MULS > 0)
-            __builtin_amdgcn_sched_group_barrier(0x020, (I + 1) * LOADS / MULS - I * LOADS / MULS, 0);
-        if constexpr ((I + 1) * READS / MULS - I * READS / MULS > 0)
-            __builtin_amdgcn_sched_group_barrier(0x100, (I + 1) * READS / MULS - I * READS / MULS, 0);
-        interleave_loads<READS, LOADS, MULS, I + 1>();
+        if constexpr (reads > 0) __builtin_amdgcn_sched_group_barrier(0x100, reads, 0);
+        if constexpr (loads > 0) __builtin_amdgcn_sched_group_barrier(0x020, loads, 0);
+        interleave<READS, LOADS, MULS, I + 1>();
     }
 }
 
-// What becomes of eight consecutive values of a product (u: the up values beside gate values v).
-template <int EPI>
-__device__ __forceinline__ void epilogue(const GemmArgs &g, int z, int m, int n, float (&v)[8], const float (&u)[8])
+// Eight consecutive values of the product stored, or added onto what is there.
+__device__ __forceinline__ void store8(const GemmArgs &g, void *c, size_t at, float (&v)[8])
 {
-    if constexpr (EPI == EPI_STORE) {
-        const size_t at = (size_t)m * g.N + n;
-        if (g.ct == DT_F32) {
-            float *p = (float *)g.c[z] + at;
-            if (g.acc) {
-                const f32x4 a = *(const f32x4 *)p, b = *(const f32x4 *)(p + 4);
+    if (g.ct == DT_F32) {
+        float *p = (float *)c + at;
+        if (g.acc) {
+            const f32x4 a = *(const f32x4 *)p, b = *(const f32x4 *)(p + 4);
 #pragma unroll
-                for (int e = 0; e < 4; e++) v[e] += a[e], v[4 + e] += b[e];
-            }
-            put8(p, v);
-        } else {
-            uint16_t *p = (uint16_t *)g.c[z] + at;
-            if (g.acc) {
-                const u32x4 b = *(const u32x4 *)p;
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    v[2 * e] += __uint_as_float(b[e] << 16);
-                    v[2 * e + 1] += __uint_as_float(b[e] & 0xFFFF0000u);
-                }
-            }
-            put_planes(p, 0, 1, v);
+            for (int e = 0; e < 4; e++) v[e] += a[e], v[4 + e] += b[e];
         }
-    } else if constexpr (EPI == EPI_GU) {
-        if (g.h) {
-            float h[8];
-#pragma unroll
-            for (int e = 0; e < 8; e++) h[e] = act_h(g.act, v[e], u[e]);
-            put_planes(g.h + (size_t)m * g.N + n, (size_t)g.M * g.N, g.planes, h);
-        }
-        if (g.gu) {
-            float *p = g.gu + (size_t)m * 2 * g.N + n;
-            put8(p, v);
-            put8(p + g.N, u);
-        }
+        put8(p, v);
     } else {
-        const float *p = g.gu + (size_t)m * 2 * g.N + n;
-        float h[8], dg[8], du[8];
-#pragma unroll
-        for (int q = 0; q < 2; q++) {
-            const f32x4 gv = *(const f32x4 *)(p + 4 * q), uv = *(const f32x4 *)(p + g.N + 4 * q);
+        uint16_t *p = (uint16_t *)c + at;
+        if (g.acc) {
+            const u32x4 b = *(const u32x4 *)p;
 #pragma unroll
             for (int e = 0; e < 4; e++) {
-                const int k = 4 * q + e;
-                act_grad(g.act, gv[e], uv[e], h[k], dg[k], du[k]);
-                dg[k] *= v[k];
-                du[k] *= v[k];
+                v[2 * e] += __uint_as_float(b[e] << 16);
+                v[2 * e + 1] += __uint_as_float(b[e] & 0xFFFF0000u);
             }
         }
-        if (g.h) put_planes(g.h + (size_t)m * g.N + n, (size_t)g.M * g.N, g.planes, h);
-        if (g.dgu) {
-            uint16_t *o = g.dgu + (size_t)m * 2 * g.N + n;
-            put_planes(o, (size_t)g.M * 2 * g.N, g.planes, dg);
-            put_planes(o + g.N, (size_t)g.M * 2 * g.N, g.planes, du);
-        }
+        put_planes(p, 0, 1, v);
     }
 }
 
-// Tile of the block's index: each XCD (blocks b % 8) takes a run of tiles, walked in groups of
-// eight row tiles so that the tiles in flight on one XCD share rows and columns in its L2.
-__device__ __forceinline__ void tile_of(int nm, int nn, int &tm, int &tn)
+// Place of tile v of the list: its product and first row and column.  Each XCD (v % 8) takes a run of the
+// list, walked in groups of eight row tiles so that the tiles in flight on one XCD share rows and
+// columns in its L2.
+struct Place {
+    int p, m0, n0;
+};
+
+template <int BM, int BNC>
+__device__ __forceinline__ Place place_of(const GemmArgs &g, int v)
 {
-    const int n = nm * nn, b = blockIdx.x, x = b & 7, j = b >> 3;
-    const int q = n >> 3, rem = n & 7;
-    const int t = x * q + min(x, rem) + j;
+    const int q = g.tiles >> 3, rem = g.tiles & 7, x = v & 7;
+    int t = x * q + min(x, rem) + (v >> 3), p = 0;
+    while (p + 1 < g.np && t >= g.p[p].tiles) t -= g.p[p++].tiles;
+    const int nm = (g.p[p].M + BM - 1) / BM, nn = (g.p[p].N + BNC - 1) / BNC;
     constexpr int kGroup = 8;
-    const int per = kGroup * nn, g = t / per, m0 = g * kGroup, gm = min(kGroup, nm - m0), r = t - g * per;
-    tm = m0 + r % gm;
-    tn = r / gm;
+    const int per = kGroup * nn, grp = t / per, first = grp * kGroup, gm = min(kGroup, nm - first), r = t - grp * per;
+    return {p, (first + r % gm) * BM, (r / gm) * BNC};
 }
 
 // WM x WN waves.  EPI_GU: the B tile holds groups of 32 rows, alternately of the gate and the up
 // matrix, so a wave's column tiles 2 j and 2 j + 1 are gate and up of the same columns.
-template <int BM, int BN, int WM, int WN, bool AK, bool BKM, int EPI>
+template <int BM, int BN, int WM, int WN, bool AK, bool BKM, int EPI, int ACT>
 __global__ __launch_bounds__(64 * WM *WN, 1) void k_ffn_gemm(GemmArgs g)
 {
     constexpr int NW = WM * WN, TM = BM / WM / 32, TN = BN / WN / 32;
     constexpr bool GU = EPI == EPI_GU;
     constexpr int BNC = GU ? BN / 2 : BN;  // output columns of a tile
     static_assert(!GU || (TN % 2 == 0 && !BKM), "gate and up tiles pair within a wave");
-    __shared__ __attribute__((aligned(1024))) uint16_t as0[BM * kBK], as1[BM * kBK], bs0[BN * kBK], bs1[BN * kBK];
+    // separate arrays, so that the compiler sees that the stream into one does not touch the other
+    __shared__ __attribute__((aligned(1024))) uint16_t as0[BM * kBK], as1[BM * kBK], as2[BM * kBK], as3[BM * kBK];
+    __shared__ __attribute__((aligned(1024))) uint16_t bs0[BN * kBK], bs1[BN * kBK], bs2[BN * kBK], bs3[BN * kBK];
+    __shared__ f32x4 scratch[NW][256];
     const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wv / WN, wn = wv % WN;
-    int tm, tn;
-    tile_of((g.M + BM - 1) / BM, (g.N + BNC - 1) / BNC, tm, tn);
-    const int m0 = tm * BM, n0 = tn * BNC, z = blockIdx.y;
 
     Tile<BM, AK, NW> ta;
     Tile<BN, BKM, NW, BNC> tb;
-    ta.init(wv, lane, g.M - m0, g.lda);
-    tb.init(wv, lane, g.N - n0, g.ldb);
-    if constexpr (GU) {
-        // tile row r: matrix r / 32 % 2, output column 32 (r / 64) + r % 32
-#pragma unroll
-        for (int i = 0; i < tb.kInstr; i++) {
-            const int r = 8 * (wv * tb.kInstr + i) + (lane >> 3), col = 32 * (r >> 6) + (r & 31);
-            const int c = (lane & 7) ^ ((r >> 1) & 7);
-            tb.voff[i] = n0 + col < g.N ? ((uint32_t)col * g.ldb + 8 * c) * 2 : kOob;
-        }
-    }
+    ta.init(wv, lane);
+    tb.init(wv, lane);
 
     f32x16 acc[TM][TN];
-#pragma unroll
-    for (int i = 0; i < TM; i++)
-#pragma unroll
-        for (int j = 0; j < TN; j++)
-#pragma unroll
-            for (int e = 0; e < 16; e++) acc[i][j][e] = 0.f;
+    bf16x8 fa[2][TM], fb[2][TN];
 
-    const int ksteps = (g.K + kBK - 1) / kBK, nsteps = ksteps * g.nseg;
-    int lseg = 0, lk = 0;  // segment and k of the next load
-    // The next tile into as, bs; after the last one zeros, so that the loop needs no branch.
-    auto load = [&](uint16_t *as, uint16_t *bs) {
-        const bool live = lseg < g.nseg;
-        const Seg s = g.seg[z][live ? lseg : 0];
-        const auto ra = ta.window(AK ? s.a + m0 : s.a + (size_t)m0 * g.lda, lk, g.K, live);
-        const auto rb = tb.window(BKM ? s.b + n0 : s.b + (size_t)n0 * g.ldb, lk, g.K, live);
+    const int ksteps = (g.K + kBK - 1) / kBK;
+    const int nsteps = (ksteps * g.nseg + kBufs - 1) & ~(kBufs - 1);  // filled up with steps of zeros
+    // The stream of loads: tile, step, segment and k of the next one, and what they read.  All of it is
+    // kept in registers: a scalar load in the loop would wait for every LDS read in flight.
+    int lv = blockIdx.x, lstep = 0, lseg = 0, lk = 0;
+    Place lp;
+    const uint16_t *pa, *pb, *pu = nullptr;
+    int lda, ldb, lefta, leftb;
+    bool live = true;
+    auto segment = [&] {
+        const Prob &p = g.p[lp.p];
+        pa = p.a[lseg] + (AK ? (size_t)lp.m0 : (size_t)lp.m0 * lda);
+        pb = p.b[lseg] + (BKM ? (size_t)lp.n0 : (size_t)lp.n0 * ldb);
+        if constexpr (GU) pu = g.b2 + (size_t)lp.n0 * ldb;
+    };
+    auto turn = [&] {
+        lp = place_of<BM, BNC>(g, lv);
+        const Prob &p = g.p[lp.p];
+        lda = p.lda, ldb = p.ldb, lefta = p.M - lp.m0, leftb = p.N - lp.n0;
+        ta.turn(lefta, lda);
+        tb.turn(leftb, ldb);
+        segment();
+    };
+    turn();
+    const int K = g.K, nseg = g.nseg, ntiles = g.tiles, nblocks = gridDim.x;
+    auto load_a = [&](uint16_t *as) {
+        const auto w = ta.window(pa, lefta, lda, lk, K, live);
 #pragma unroll
-        for (int i = 0; i < ta.kInstr; i++) ta.piece(ra, as, i, lk, g.K, wv, lane);
+        for (int i = 0; i < ta.kInstr; i++) ta.piece(w, as, i, K - lk, wv);
+    };
+    auto load_b = [&](uint16_t *bs) {
+        const auto w = tb.window(pb, leftb, ldb, lk, K, live);
         if constexpr (GU) {
-            const auto ru = tb.window(g.b2 + (size_t)n0 * g.ldb, lk, g.K, live);
+            const auto wu = tb.window(pu, leftb, ldb, lk, K, live);
 #pragma unroll
-            for (int i = 0; i < tb.kInstr; i++)  // eight rows, all of one matrix
-                tb.piece(((wv * tb.kInstr + i) >> 2) & 1 ? ru : rb, bs, i, lk, g.K, wv, lane);
+            for (int i = 0; i < tb.kInstr; i++)  // sixteen rows, all of one matrix
+                tb.piece(((wv * tb.kInstr + i) >> 1) & 1 ? wu : w, bs, i, K - lk, wv);
         } else {
 #pragma unroll
-            for (int i = 0; i < tb.kInstr; i++) tb.piece(rb, bs, i, lk, g.K, wv, lane);
+            for (int i = 0; i < tb.kInstr; i++) tb.piece(w, bs, i, K - lk, wv);
         }
+    };
+    auto advance = [&] {
         lk += kBK;
-        const bool over = lk >= g.K;
-        lk = over ? 0 : lk;
-        lseg += over;
+        lstep++;
+        if (lk < K && lstep < nsteps) return;
+        lk = 0;
+        if (lstep == nsteps) {
+            lstep = lseg = 0;
+            lv += nblocks;
+            live = lv < ntiles;
+            if (live) turn();
+        } else if (++lseg < nseg) {
+            segment();
+        } else {
+            live = false;  // steps of zeros up to a multiple of kBufs
+        }
     };
     // Fragments of the 16 reduction indices s of a tile.
-    bf16x8 fa[2][TM], fb[2][TN];
     auto read = [&](auto P, const uint16_t *as, const uint16_t *bs, int s) {
         constexpr int p = decltype(P)::value;
 #pragma unroll
-        for (int j = 0; j < TN; j++) fb[p][j] = Tile<BN, BKM, NW>::frag(bs, 32 * (wn * TN + j), s, lane);
+        for (int j = 0; j < TN; j++) fb[p][j] = Tile<BN, BKM, NW, BNC>::frag(bs, 32 * (wn * TN + j), s, lane);
 #pragma unroll
         for (int i = 0; i < TM; i++) fa[p][i] = Tile<BM, AK, NW>::frag(as, 32 * (wm * TM + i), s, lane);
     };
@@ -381,116 +438,215 @@ __global__ __launch_bounds__(64 * WM *WN, 1) void k_ffn_gemm(GemmArgs g)
     using E = std::integral_constant<int, 0>;
     using O = std::integral_constant<int, 1>;
     constexpr int kReads = TN * (BKM ? 2 : 1) + TM * (AK ? 2 : 1), kMul = TM * TN;
-    // One tile of 64 k: the fragments of the next 16 k are read while the present ones are multiplied.
-    // One barrier a tile, before its last 16 k: by then every wave has read all of this buffer (so the
-    // tile after next may stream into it) and has seen its own part of the next tile arrive.
-    auto step = [&](const uint16_t *as, const uint16_t *bs, uint16_t *lda_, uint16_t *ldb_, const uint16_t *an, const uint16_t *bn) {
+    // One step of 32 k.  The fragments of the next 16 k are read while the present ones are multiplied, and
+    // the loads of the step three further on are spread evenly over the matrix instructions (issued in a
+    // bunch they fill the memory pipe's queue, and the wave that waits to issue the next one issues no
+    // matrix instruction either).  One barrier a step, before its last 16 k: by then every wave has read
+    // all of this buffer (the loads of the next step's turn may stream into it) and has seen its own part
+    // of the next step arrive (all but the newest loads: a step's, and half of another's).
+    auto step = [&](const uint16_t *as, const uint16_t *bs, const uint16_t *an, const uint16_t *bn, uint16_t *al, uint16_t *bl) {
+        load_a(al);
         read(O(), as, bs, 1);
         mul(E());
-        interleave<kReads, kMul>();
-        read(E(), as, bs, 2);
+        interleave<kReads, ta.kInstr, kMul>();
+        wait_vm<2 * ta.kInstr + tb.kInstr>();
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        load_b(bl);
+        read(E(), an, bn, 0);
         mul(O());
-        interleave<kReads, kMul>();
-        read(O(), as, bs, 3);
-        mul(E());
-        interleave<kReads, kMul>();
-        wait_vm<0>();
-        __syncthreads();
-        load(lda_, ldb_);
-        read(E(), an, bn, 0);  // past the last tile: zeros, not used
-        mul(O());
-        interleave_loads<kReads, ta.kInstr + tb.kInstr, kMul>();
+        interleave<kReads, tb.kInstr, kMul>();
+        advance();
     };
 
-    load(as0, bs0);
-    load(as1, bs1);
-    wait_vm<0>();
-    __syncthreads();
+    load_a(as0);
+    load_b(bs0);
+    advance();
+    load_a(as1);
+    load_b(bs1);
+    advance();
+    load_a(as2);
+    load_b(bs2);
+    advance();
+    wait_vm<2 * (ta.kInstr + tb.kInstr)>();
+    asm volatile("s_barrier" ::: "memory");
     read(E(), as0, bs0, 0);
-    int st = 0;
-    for (; st + 2 <= nsteps; st += 2) {
-        step(as0, bs0, as0, bs0, as1, bs1);
-        step(as1, bs1, as1, bs1, as0, bs0);
-    }
-    if (st < nsteps) step(as0, bs0, as0, bs0, as1, bs1);
-    wait_vm<0>();  // the zeros behind the last tile have landed before the epilogue uses the buffers
-    __syncthreads();
 
-    // Epilogue: a wave's 32 x 64 part at a time goes through its own 8 KB of LDS (16-byte chunk c of a
-    // row at c ^ (row % 16)), so that a lane ends up with eight consecutive columns of a row and the
-    // stores cover whole lines; the loop over the rows stays rolled.
-    uint16_t *const pool[4] = {as0, as1, bs0, bs1};
-    constexpr int kPer = NW > 4 ? NW / 4 : 1;
-    static_assert(TN % 2 == 0 && kPer * 8192 <= BM * kBK * 2 && kPer * 8192 <= BN * kBK * 2, "epilogue scratch");
-    uint16_t *slot = as0;
+    f32x4 *const sc = scratch[wv];
+    const int lr = lane >> 2, lc = lane & 3;  // row (of 16) and group of eight columns of the epilogue
+    for (int v = blockIdx.x; v < g.tiles; v += gridDim.x) {
+        const Place at = place_of<BM, BNC>(g, v);
+        const int M = g.p[at.p].M, N = g.p[at.p].N;
+        const int mw = at.m0 + 32 * wm * TM, nw = at.n0 + (GU ? 16 : 32) * wn * TN;
 #pragma unroll
-    for (int k = 1; k < 4; k++)
-        if (wv / kPer == k) slot = pool[k];
-    f32x4 *const sc = (f32x4 *)(slot + 4096 * (wv % kPer));
+        for (int i = 0; i < TM; i++)
 #pragma unroll
-    for (int i = 0; i < TM; i++)
+            for (int j = 0; j < TN; j++)
 #pragma unroll
-        for (int j = 0; j < TN; j += 2) {
-            wave_fence();
-#pragma unroll
-            for (int d = 0; d < 2; d++)
-#pragma unroll
-                for (int q = 0; q < 4; q++) {
-                    const int m = lane & 31, c = 8 * d + 2 * q + (lane >> 5);
-                    sc[16 * m + (c ^ (m & 15))] = f32x4{acc[i][j + d][4 * q], acc[i][j + d][4 * q + 1], acc[i][j + d][4 * q + 2], acc[i][j + d][4 * q + 3]};
-                }
-            wave_fence();
-            const int mb = m0 + 32 * (wm * TM + i);
-            const int nb = GU ? n0 + 16 * (wn * TN + j) : n0 + 32 * (wn * TN + j);
-            constexpr int lpr = GU ? 4 : 8;  // lanes per row
-#pragma unroll 1
-            for (int r0 = 0; r0 < 32; r0 += 64 / lpr) {
-                const int r = r0 + lane / lpr, cb = lane % lpr, m = mb + r, n = nb + 8 * cb;
-                float v[8], u[8];
-                get8(sc, r, cb, v);
-                if constexpr (GU) get8(sc, r, 4 + cb, u);
-                if (m < g.M && n < g.N) epilogue<EPI>(g, z, m, n, v, u);
-            }
+                for (int e = 0; e < 16; e++) acc[i][j][e] = 0.f;
+        for (int st = 0; st < nsteps; st += kBufs) {
+            step(as0, bs0, as1, bs1, as3, bs3);
+            step(as1, bs1, as2, bs2, as0, bs0);
+            step(as2, bs2, as3, bs3, as1, bs1);
+            step(as3, bs3, as0, bs0, as2, bs2);
         }
+
+        // f(row, column, eight values) for each part of the 32 x 32 tile whose value of element e is value(e)
+        auto rows = [&](int mb, int nb, auto &&value, auto &&f) {
+            wave_fence();
+            put_tile(sc, lane, value);
+            wave_fence();
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const int r = 16 * h + lr;
+                float x[8];
+                get8(sc, r, lc, x);
+                if (mb + r < M && nb + 8 * lc < N) f(h, mb + r, nb + 8 * lc, x);
+            }
+        };
+        if constexpr (EPI == EPI_STORE) {
+            void *const c = g.p[at.p].c;
+            each<TM * TN>([&](auto B) {
+                constexpr int i = B.value / TN, j = B.value % TN;
+                rows(mw + 32 * i, nw + 32 * j, [&](int e) { return acc[i][j][e]; },
+                     [&](int, int m, int n, float (&x)[8]) { store8(g, c, (size_t)m * N + n, x); });
+            });
+        } else if constexpr (GU) {
+            each<TM * TN / 2>([&](auto B) {
+                constexpr int i = B.value / (TN / 2), j = 2 * (B.value % (TN / 2));
+                const int mb = mw + 32 * i, nb = nw + 16 * j;
+                float gx[2][8];
+                rows(mb, nb, [&](int e) { return acc[i][j][e]; },
+                     [&](int h, int, int, float (&x)[8]) {
+#pragma unroll
+                         for (int e = 0; e < 8; e++) gx[h][e] = x[e];
+                     });
+                rows(mb, nb, [&](int e) { return acc[i][j + 1][e]; },
+                     [&](int h, int m, int n, float (&x)[8]) {
+                         if (g.gu) {
+                             float *p = g.gu + (size_t)m * 2 * N + n;
+                             put8(p, gx[h]);
+                             put8(p + N, x);
+                         }
+#pragma unroll
+                         for (int e = 0; e < 8; e++) x[e] = gated<ACT>(gx[h][e], x[e]);
+                         if (g.h) put_planes(g.h + (size_t)m * N + n, (size_t)M * N, g.planes, x);
+                     });
+            });
+        } else {
+            // the saved g and u of the next 32 x 32 tile are requested before the present one is worked on
+            f32x4 gv[2][2][2], uv[2][2][2];
+            auto fetch = [&](auto P, int mb, int nb) {
+                constexpr int p = decltype(P)::value;
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    const int m = min(mb + 16 * h + lr, M - 1), n = min(nb + 8 * lc, N - 8);
+                    const float *s = g.gu + (size_t)m * 2 * N + n;
+#pragma unroll
+                    for (int q = 0; q < 2; q++) {
+                        gv[p][h][q] = *(const f32x4 *)(s + 4 * q);
+                        uv[p][h][q] = *(const f32x4 *)(s + N + 4 * q);
+                    }
+                }
+            };
+            fetch(E(), mw, nw);
+            each<TM * TN>([&](auto B) {
+                constexpr int i = B.value / TN, j = B.value % TN, p = B.value & 1, k = B.value + 1;
+                if constexpr (k < TM * TN) fetch(std::integral_constant<int, 1 - p>(), mw + 32 * (k / TN), nw + 32 * (k % TN));
+                rows(mw + 32 * i, nw + 32 * j, [&](int e) { return acc[i][j][e]; },
+                     [&](int h, int m, int n, float (&x)[8]) {
+                         float hv[8], dg[8], du[8];
+#pragma unroll
+                         for (int e = 0; e < 8; e++) {
+                             gated_grad<ACT>(gv[p][h][e >> 2][e & 3], uv[p][h][e >> 2][e & 3], hv[e], dg[e], du[e]);
+                             dg[e] *= x[e];
+                             du[e] *= x[e];
+                         }
+                         if (g.h) put_planes(g.h + (size_t)m * N + n, (size_t)M * N, g.planes, hv);
+                         if (g.dgu) {
+                             uint16_t *o = g.dgu + (size_t)m * 2 * N + n;
+                             put_planes(o, (size_t)M * 2 * N, g.planes, dg);
+                             put_planes(o + N, (size_t)M * 2 * N, g.planes, du);
+                         }
+                     });
+            });
+        }
+    }
 }
 
-template <int BM, int BN, int WM, int WN, bool AK, bool BKM, int EPI>
-hipError_t go(const GemmArgs &g, int nz, hipStream_t s)
+// Compute units of the current device.
+int compute_units()
+{
+    int dev = 0, n = 0;
+    if (hipGetDevice(&dev) != hipSuccess || hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0) return 256;
+    return n;
+}
+
+template <int BM, int BN, int EPI>
+int64_t count_tiles(GemmArgs &g)
 {
     constexpr int BNC = EPI == EPI_GU ? BN / 2 : BN;
-    const size_t tiles = (size_t)((g.M + BM - 1) / BM) * ((g.N + BNC - 1) / BNC);
-    hipLaunchKernelGGL((k_ffn_gemm<BM, BN, WM, WN, AK, BKM, EPI>), dim3((unsigned)tiles, (unsigned)nz), dim3(64 * WM * WN), 0, s, g);
+    int64_t n = 0;
+    for (int i = 0; i < g.np; i++) {
+        const int64_t t = (int64_t)((g.p[i].M + BM - 1) / BM) * ((g.p[i].N + BNC - 1) / BNC);
+        g.p[i].tiles = (int)t;
+        n += t;
+    }
+    g.tiles = (int)n;
+    return n;
+}
+
+// per_cu: blocks that fit a compute unit's LDS (a multiple of 8 blocks keeps a block's tiles on one XCD)
+template <int BM, int BN, int WM, int WN, bool AK, bool BKM, int EPI, int ACT>
+hipError_t go(GemmArgs g, int per_cu, int cus, hipStream_t s)
+{
+    const int64_t tiles = count_tiles<BM, BN, EPI>(g);
+    if (tiles > (int64_t)1 << 30) return hipErrorInvalidValue;
+    const int slots = per_cu * cus >= 8 ? per_cu * cus & ~7 : 8;
+    const unsigned grid = (unsigned)(tiles < slots ? tiles : slots);
+    hipLaunchKernelGGL((k_ffn_gemm<BM, BN, WM, WN, AK, BKM, EPI, ACT>), dim3(grid), dim3(64 * WM * WN), 0, s, g);
     return hipGetLastError();
 }
 
-template <bool AK, bool BKM, int EPI>
-hipError_t gemm(const GemmArgs &g, int nz, hipStream_t s)
+template <bool AK, bool BKM, int EPI, int ACT = 0>
+hipError_t gemm(GemmArgs g, hipStream_t s)
 {
-    constexpr int cols = EPI == EPI_GU ? 2 : 1;
-    const size_t big = (size_t)((g.M + 255) / 256) * ((cols * (size_t)g.N + 255) / 256) * nz;
-    if (big >= 200) return go<256, 256, 2, 2, AK, BKM, EPI>(g, nz, s);
-    const size_t mid = (size_t)((g.M + 127) / 128) * ((cols * (size_t)g.N + 127) / 128) * nz;
-    if (mid >= 200) return go<128, 128, 2, 2, AK, BKM, EPI>(g, nz, s);
-    return go<64, 64, 2, 1, AK, BKM, EPI>(g, nz, s);
+    const int cus = compute_units();
+    if (count_tiles<256, 256, EPI>(g) >= 200) return go<256, 256, 2, 2, AK, BKM, EPI, ACT>(g, 1, cus, s);
+    if (count_tiles<128, 128, EPI>(g) >= 200) return go<128, 128, 2, 2, AK, BKM, EPI, ACT>(g, 2, cus, s);
+    return go<64, 64, 2, 1, AK, BKM, EPI, ACT>(g, 4, cus, s);
+}
+
+// Product i of g.
+Prob &prob(GemmArgs &g, int M, int N, int lda, int ldb, void *c)
+{
+    Prob &p = g.p[g.np++];
+    p.M = M, p.N = N, p.lda = lda, p.ldb = ldb, p.c = c;
+    return p;
 }
 
 }  // namespace
 
+// g and u (kept in gu unless null), h in `planes` terms unless null
+static hipError_t gate_up(const FfnArgs &a, uint16_t *h, int planes, float *gu, hipStream_t s)
+{
+    GemmArgs g{};
+    Prob &p = prob(g, a.T, a.I, a.D, a.D, nullptr);
+    g.nseg = 1, g.K = a.D;
+    p.a[0] = a.x, p.b[0] = a.wg, g.b2 = a.wu;
+    g.planes = planes, g.h = h, g.gu = gu;
+    return a.act == ACT_SITU ? gemm<false, false, EPI_GU, ACT_SITU>(g, s) : gemm<false, false, EPI_GU, ACT_SWIGLU>(g, s);
+}
+
 hipError_t launch_ffn_forward(const FfnArgs &a, hipStream_t s)
 {
     const int planes = a.yt == DT_F32 ? kFfnPlanes : 1;
-    GemmArgs g{};
-    g.M = a.T, g.N = a.I, g.K = a.D, g.lda = g.ldb = a.D, g.nseg = 1;
-    g.seg[0][0] = {a.x, a.wg};
-    g.b2 = a.wu;
-    g.act = a.act, g.planes = planes, g.h = a.h, g.gu = a.gu;
-    hipError_t e = gemm<false, false, EPI_GU>(g, 1, s);
+    const hipError_t e = gate_up(a, a.h, planes, a.gu, s);
     if (e != hipSuccess) return e;
-    GemmArgs d{};
-    d.M = a.T, d.N = a.D, d.K = a.I, d.lda = d.ldb = a.I, d.nseg = planes;
-    for (int p = 0; p < planes; p++) d.seg[0][p] = {a.h + (size_t)p * a.T * a.I, a.wd};
-    d.c[0] = a.y, d.ct = a.yt, d.acc = a.acc;
-    return gemm<false, false, EPI_STORE>(d, 1, s);
+    GemmArgs g{};
+    Prob &p = prob(g, a.T, a.D, a.I, a.I, a.y);
+    g.nseg = planes, g.K = a.I, g.ct = a.yt, g.acc = a.acc;
+    for (int k = 0; k < planes; k++) p.a[k] = a.h + (size_t)k * a.T * a.I, p.b[k] = a.wd;
+    return gemm<false, false, EPI_STORE>(g, s);
 }
 
 hipError_t launch_ffn_backward(const FfnArgs &a, hipStream_t s)
@@ -502,52 +658,44 @@ hipError_t launch_ffn_backward(const FfnArgs &a, hipStream_t s)
     const float *gu = a.saved_gu;
     hipError_t e;
     if (!gu) {
-        GemmArgs g{};
-        g.M = a.T, g.N = a.I, g.K = a.D, g.lda = g.ldb = a.D, g.nseg = 1;
-        g.seg[0][0] = {a.x, a.wg};
-        g.b2 = a.wu;
-        g.act = a.act, g.planes = 1, g.gu = a.gu_ws;
-        if ((e = gemm<false, false, EPI_GU>(g, 1, s)) != hipSuccess) return e;
+        if ((e = gate_up(a, nullptr, 1, a.gu_ws, s)) != hipSuccess) return e;
         gu = a.gu_ws;
     }
     {
         GemmArgs g{};
-        g.M = a.T, g.N = a.I, g.K = a.D, g.lda = a.D, g.ldb = a.I, g.nseg = 1;
-        g.seg[0][0] = {a.dy, a.wd};
-        g.act = a.act, g.planes = px > pw ? px : pw, g.gu = const_cast<float *>(gu);
+        Prob &p = prob(g, a.T, a.I, a.D, a.I, nullptr);
+        g.nseg = 1, g.K = a.D;
+        p.a[0] = a.dy, p.b[0] = a.wd;
+        g.planes = px > pw ? px : pw, g.gu = const_cast<float *>(gu);
         g.h = a.dwd ? a.h : nullptr;
         g.dgu = a.dx || dwgu ? a.dgu : nullptr;
-        if ((e = gemm<false, true, EPI_DGU>(g, 1, s)) != hipSuccess) return e;
+        e = a.act == ACT_SITU ? gemm<false, true, EPI_DGU, ACT_SITU>(g, s) : gemm<false, true, EPI_DGU, ACT_SWIGLU>(g, s);
+        if (e != hipSuccess) return e;
     }
     if (a.dx) {
         GemmArgs g{};
-        g.M = a.T, g.N = a.D, g.K = a.I, g.lda = 2 * a.I, g.ldb = a.D, g.nseg = 2 * px;
-        for (int p = 0; p < px; p++) {
-            g.seg[0][2 * p] = {a.dgu + p * T * 2 * I, a.wg};
-            g.seg[0][2 * p + 1] = {a.dgu + p * T * 2 * I + I, a.wu};
+        Prob &p = prob(g, a.T, a.D, 2 * a.I, a.D, a.dx);
+        g.nseg = 2 * px, g.K = a.I, g.ct = a.dxt, g.acc = a.acc;
+        for (int k = 0; k < px; k++) {
+            p.a[2 * k] = a.dgu + k * T * 2 * I, p.b[2 * k] = a.wg;
+            p.a[2 * k + 1] = a.dgu + k * T * 2 * I + I, p.b[2 * k + 1] = a.wu;
         }
-        g.c[0] = a.dx, g.ct = a.dxt, g.acc = a.acc;
-        if ((e = gemm<false, true, EPI_STORE>(g, 1, s)) != hipSuccess) return e;
+        if ((e = gemm<false, true, EPI_STORE>(g, s)) != hipSuccess) return e;
     }
-    if (dwgu) {
+    if (pw) {
         GemmArgs g{};
-        g.M = a.I, g.N = a.D, g.K = a.T, g.lda = 2 * a.I, g.ldb = a.D, g.nseg = pw;
-        int nz = 0;
+        g.nseg = pw, g.K = a.T, g.ct = a.dwt;
         for (int m = 0; m < 2; m++) {
             void *out = m ? a.dwu : a.dwg;
             if (!out) continue;
-            for (int p = 0; p < pw; p++) g.seg[nz][p] = {a.dgu + p * T * 2 * I + m * I, a.x};
-            g.c[nz++] = out;
+            Prob &p = prob(g, a.I, a.D, 2 * a.I, a.D, out);
+            for (int k = 0; k < pw; k++) p.a[k] = a.dgu + k * T * 2 * I + m * I, p.b[k] = a.x;
         }
-        g.ct = a.dwt;
-        if ((e = gemm<true, true, EPI_STORE>(g, nz, s)) != hipSuccess) return e;
-    }
-    if (a.dwd) {
-        GemmArgs g{};
-        g.M = a.D, g.N = a.I, g.K = a.T, g.lda = a.D, g.ldb = a.I, g.nseg = pw;
-        for (int p = 0; p < pw; p++) g.seg[0][p] = {a.dy, a.h + p * T * I};
-        g.c[0] = a.dwd, g.ct = a.dwt;
-        if ((e = gemm<true, true, EPI_STORE>(g, 1, s)) != hipSuccess) return e;
+        if (a.dwd) {
+            Prob &p = prob(g, a.D, a.I, a.D, a.I, a.dwd);
+            for (int k = 0; k < pw; k++) p.a[k] = a.dy, p.b[k] = a.h + k * T * I;
+        }
+        return gemm<true, true, EPI_STORE>(g, s);
     }
     return hipSuccess;
 }
