@@ -70,8 +70,11 @@ moe_status check_overlap(std::initializer_list<Buf> outs, std::initializer_list<
 constexpr int kMaxFfnWidth = 1 << 20;
 
 struct FfnLayout {
-    size_t h, dgu, gu, total;
+    size_t h, dgu, gu, part, part_floats, total;
 };
+
+// Floats for the parts of a cut reduction: sixteen parts of the largest output, at most 64 MB.
+constexpr size_t kPartFloats = (size_t)16 << 20;
 
 FfnLayout ffn_layout(const moe_ffn_desc &d)
 {
@@ -87,6 +90,9 @@ FfnLayout ffn_layout(const moe_ffn_desc &d)
     L.h = take(moe::kFfnPlanes * T * I * 2);
     L.dgu = take(back ? moe::kFfnPlanes * T * 2 * I * 2 : 0);
     L.gu = take(back ? T * 2 * I * 4 : 0);
+    const size_t D = d.width, most = std::max({T * 2 * I, T * D, back ? 3 * D * I : 0});
+    L.part_floats = std::min(16 * most, kPartFloats);
+    L.part = take(L.part_floats * 4);
     L.total = off;
     return L;
 }
@@ -221,6 +227,8 @@ moe::FfnArgs ffn_args(const moe_ffn *f, const uint16_t *x, int32_t T)
     a.h = (uint16_t *)(f->ws + f->lay.h);
     a.dgu = (uint16_t *)(f->ws + f->lay.dgu);
     a.gu_ws = (float *)(f->ws + f->lay.gu);
+    a.part = (float *)(f->ws + f->lay.part);
+    a.part_floats = f->lay.part_floats;
     return a;
 }
 

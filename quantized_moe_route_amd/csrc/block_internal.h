@@ -98,6 +98,8 @@ struct FfnArgs {
     uint16_t *h;     // [planes][T][I]
     uint16_t *dgu;   // [planes][T][2I]
     float *gu_ws;    // [T][2][I], used where saved_gu is missing
+    float *part;     // parts of a reduction that is cut
+    size_t part_floats;
     // backward
     const uint16_t *dy;
     const float *saved_gu;

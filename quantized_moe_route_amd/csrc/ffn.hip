@@ -42,13 +42,16 @@ struct Prob {
     int tiles;           // number of output tiles (set by the launcher)
     const uint16_t *a[kMaxSeg], *b[kMaxSeg];
     void *c;             // EPI_STORE
+    float *part;         // the reduction cut in parts: [splits][M][N], of EPI_GU [splits][M][2N]
 };
 
 // Up to three products with the same reduction, walked as one list of tiles.
 struct GemmArgs {
     Prob p[3];
     int np, nseg, K;      // K: reduction length of each segment
-    int tiles;
+    int tiles;            // of all products, times splits (set by the launcher, as the next two)
+    int splits;           // parts of the reduction, each a tile of its own in the list
+    int steps;            // steps of a part, a multiple of kBufs
     const uint16_t *b2;   // EPI_GU: the up matrix (b of the segment is the gate matrix)
     int ct;               // EPI_STORE: dtype of c
     bool acc;
@@ -317,11 +320,48 @@ __device__ __forceinline__ void store8(const GemmArgs &g, void *c, size_t at, fl
     }
 }
 
+// Eight consecutive gate and up values: kept, and their h.
+template <int ACT>
+__device__ __forceinline__ void gate8(const GemmArgs &g, int M, int N, int m, int n, const float (&gg)[8], const float (&uu)[8])
+{
+    if (g.gu) {
+        float *p = g.gu + (size_t)m * 2 * N + n;
+        put8(p, gg);
+        put8(p + N, uu);
+    }
+    if (g.h) {
+        float h[8];
+#pragma unroll
+        for (int e = 0; e < 8; e++) h[e] = gated<ACT>(gg[e], uu[e]);
+        put_planes(g.h + (size_t)m * N + n, (size_t)M * N, g.planes, h);
+    }
+}
+
+// Eight consecutive values of d h with their saved g and u: h, dg and du.
+template <int ACT>
+__device__ __forceinline__ void back8(const GemmArgs &g, int M, int N, int m, int n, const float (&dh)[8], const float (&gg)[8],
+                                      const float (&uu)[8])
+{
+    float h[8], dg[8], du[8];
+#pragma unroll
+    for (int e = 0; e < 8; e++) {
+        gated_grad<ACT>(gg[e], uu[e], h[e], dg[e], du[e]);
+        dg[e] *= dh[e];
+        du[e] *= dh[e];
+    }
+    if (g.h) put_planes(g.h + (size_t)m * N + n, (size_t)M * N, g.planes, h);
+    if (g.dgu) {
+        uint16_t *o = g.dgu + (size_t)m * 2 * N + n;
+        put_planes(o, (size_t)M * 2 * N, g.planes, dg);
+        put_planes(o + N, (size_t)M * 2 * N, g.planes, du);
+    }
+}
+
 // Place of tile v of the list: its product and first row and column.  Each XCD (v % 8) takes a run of the
 // list, walked in groups of eight row tiles so that the tiles in flight on one XCD share rows and
 // columns in its L2.
 struct Place {
-    int p, m0, n0;
+    int p, m0, n0, part;
 };
 
 template <int BM, int BNC>
@@ -329,11 +369,13 @@ __device__ __forceinline__ Place place_of(const GemmArgs &g, int v)
 {
     const int q = g.tiles >> 3, rem = g.tiles & 7, x = v & 7;
     int t = x * q + min(x, rem) + (v >> 3), p = 0;
+    const int part = t % g.splits;
+    t /= g.splits;
     while (p + 1 < g.np && t >= g.p[p].tiles) t -= g.p[p++].tiles;
     const int nm = (g.p[p].M + BM - 1) / BM, nn = (g.p[p].N + BNC - 1) / BNC;
     constexpr int kGroup = 8;
     const int per = kGroup * nn, grp = t / per, first = grp * kGroup, gm = min(kGroup, nm - first), r = t - grp * per;
-    return {p, (first + r % gm) * BM, (r / gm) * BNC};
+    return {p, (first + r % gm) * BM, (r / gm) * BNC, part};
 }
 
 // WM x WN waves.  EPI_GU: the B tile holds groups of 32 rows, alternately of the gate and the up
@@ -360,8 +402,7 @@ __global__ __launch_bounds__(64 * WM *WN, 1) void k_ffn_gemm(GemmArgs g)
     f32x16 acc[TM][TN];
     bf16x8 fa[2][TM], fb[2][TN];
 
-    const int ksteps = (g.K + kBK - 1) / kBK;
-    const int nsteps = (ksteps * g.nseg + kBufs - 1) & ~(kBufs - 1);  // filled up with steps of zeros
+    const int ksteps = (g.K + kBK - 1) / kBK, nsteps = g.steps;  // filled up with steps of zeros
     // The stream of loads: tile, step, segment and k of the next one, and what they read.  All of it is
     // kept in registers: a scalar load in the loop would wait for every LDS read in flight.
     int lv = blockIdx.x, lstep = 0, lseg = 0, lk = 0;
@@ -381,7 +422,11 @@ __global__ __launch_bounds__(64 * WM *WN, 1) void k_ffn_gemm(GemmArgs g)
         lda = p.lda, ldb = p.ldb, lefta = p.M - lp.m0, leftb = p.N - lp.n0;
         ta.turn(lefta, lda);
         tb.turn(leftb, ldb);
-        segment();
+        const int first = lp.part * nsteps;
+        lseg = first / ksteps;
+        lk = (first - lseg * ksteps) * kBK;
+        live = lseg < g.nseg;
+        if (live) segment();
     };
     turn();
     const int K = g.K, nseg = g.nseg, ntiles = g.tiles, nblocks = gridDim.x;
@@ -406,16 +451,15 @@ __global__ __launch_bounds__(64 * WM *WN, 1) void k_ffn_gemm(GemmArgs g)
         lk += kBK;
         lstep++;
         if (lk < K && lstep < nsteps) return;
-        lk = 0;
         if (lstep == nsteps) {
-            lstep = lseg = 0;
+            lstep = lk = 0;
             lv += nblocks;
             live = lv < ntiles;
             if (live) turn();
-        } else if (++lseg < nseg) {
-            segment();
         } else {
-            live = false;  // steps of zeros up to a multiple of kBufs
+            lk = 0;
+            live = ++lseg < nseg;  // past the last segment: steps of zeros up to the part's length
+            if (live) segment();
         }
     };
     // Fragments of the 16 reduction indices s of a tile.
@@ -503,6 +547,18 @@ __global__ __launch_bounds__(64 * WM *WN, 1) void k_ffn_gemm(GemmArgs g)
                 if (mb + r < M && nb + 8 * lc < N) f(h, mb + r, nb + 8 * lc, x);
             }
         };
+        if (g.splits > 1) {
+            // the part's sums as they are, for k_ffn_join
+            const int W = GU ? 2 * N : N;
+            float *const part = g.p[at.p].part + (size_t)at.part * M * W;
+            each<TM * TN>([&](auto B) {
+                constexpr int i = B.value / TN, j = B.value % TN;
+                const int nb = GU ? nw + 16 * (j & ~1) : nw + 32 * j;
+                rows(mw + 32 * i, nb, [&](int e) { return acc[i][j][e]; },
+                     [&](int, int m, int n, float (&x)[8]) { put8(part + (size_t)m * W + (GU && (j & 1) ? N : 0) + n, x); });
+            });
+            continue;
+        }
         if constexpr (EPI == EPI_STORE) {
             void *const c = g.p[at.p].c;
             each<TM * TN>([&](auto B) {
@@ -522,14 +578,7 @@ __global__ __launch_bounds__(64 * WM *WN, 1) void k_ffn_gemm(GemmArgs g)
                      });
                 rows(mb, nb, [&](int e) { return acc[i][j + 1][e]; },
                      [&](int h, int m, int n, float (&x)[8]) {
-                         if (g.gu) {
-                             float *p = g.gu + (size_t)m * 2 * N + n;
-                             put8(p, gx[h]);
-                             put8(p + N, x);
-                         }
-#pragma unroll
-                         for (int e = 0; e < 8; e++) x[e] = gated<ACT>(gx[h][e], x[e]);
-                         if (g.h) put_planes(g.h + (size_t)m * N + n, (size_t)M * N, g.planes, x);
+                         gate8<ACT>(g, M, N, m, n, gx[h], x);
                      });
             });
         } else {
@@ -554,19 +603,10 @@ __global__ __launch_bounds__(64 * WM *WN, 1) void k_ffn_gemm(GemmArgs g)
                 if constexpr (k < TM * TN) fetch(std::integral_constant<int, 1 - p>(), mw + 32 * (k / TN), nw + 32 * (k % TN));
                 rows(mw + 32 * i, nw + 32 * j, [&](int e) { return acc[i][j][e]; },
                      [&](int h, int m, int n, float (&x)[8]) {
-                         float hv[8], dg[8], du[8];
+                         float gg[8], uu[8];
 #pragma unroll
-                         for (int e = 0; e < 8; e++) {
-                             gated_grad<ACT>(gv[p][h][e >> 2][e & 3], uv[p][h][e >> 2][e & 3], hv[e], dg[e], du[e]);
-                             dg[e] *= x[e];
-                             du[e] *= x[e];
-                         }
-                         if (g.h) put_planes(g.h + (size_t)m * N + n, (size_t)M * N, g.planes, hv);
-                         if (g.dgu) {
-                             uint16_t *o = g.dgu + (size_t)m * 2 * N + n;
-                             put_planes(o, (size_t)M * 2 * N, g.planes, dg);
-                             put_planes(o + N, (size_t)M * 2 * N, g.planes, du);
-                         }
+                         for (int e = 0; e < 8; e++) gg[e] = gv[p][h][e >> 2][e & 3], uu[e] = uv[p][h][e >> 2][e & 3];
+                         back8<ACT>(g, M, N, m, n, x, gg, uu);
                      });
             });
         }
@@ -581,6 +621,45 @@ int compute_units()
     return n;
 }
 
+// Joins the parts of product blockIdx.y in order, eight columns a thread, and finishes it.
+template <int EPI, int ACT>
+__global__ __launch_bounds__(256) void k_ffn_join(GemmArgs g)
+{
+    constexpr bool GU = EPI == EPI_GU;
+    const Prob &p = g.p[blockIdx.y];
+    const int M = p.M, N = p.N, W = GU ? 2 * N : N, per = N / 8;
+    const size_t stride = (size_t)M * W, total = (size_t)M * per;
+    for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (size_t)gridDim.x * 256) {
+        const int m = (int)(i / per), n = 8 * (int)(i % per);
+        const float *src = p.part + (size_t)m * W + n;
+        float v[8], u[8];
+#pragma unroll
+        for (int e = 0; e < 8; e++) v[e] = u[e] = 0.f;
+        for (int s = 0; s < g.splits; s++) {
+            const float *q = src + s * stride;
+            const f32x4 a = *(const f32x4 *)q, b = *(const f32x4 *)(q + 4);
+#pragma unroll
+            for (int e = 0; e < 4; e++) v[e] += a[e], v[4 + e] += b[e];
+            if constexpr (GU) {
+                const f32x4 c = *(const f32x4 *)(q + N), d = *(const f32x4 *)(q + N + 4);
+#pragma unroll
+                for (int e = 0; e < 4; e++) u[e] += c[e], u[4 + e] += d[e];
+            }
+        }
+        if constexpr (EPI == EPI_STORE) {
+            store8(g, p.c, (size_t)m * N + n, v);
+        } else if constexpr (GU) {
+            gate8<ACT>(g, M, N, m, n, v, u);
+        } else {
+            const float *q = g.gu + (size_t)m * 2 * N + n;
+            float gg[8];
+#pragma unroll
+            for (int e = 0; e < 8; e++) gg[e] = q[e], u[e] = q[N + e];
+            back8<ACT>(g, M, N, m, n, v, gg, u);
+        }
+    }
+}
+
 template <int BM, int BN, int EPI>
 int64_t count_tiles(GemmArgs &g)
 {
@@ -591,29 +670,84 @@ int64_t count_tiles(GemmArgs &g)
         g.p[i].tiles = (int)t;
         n += t;
     }
-    g.tiles = (int)n;
     return n;
 }
 
-// per_cu: blocks that fit a compute unit's LDS (a multiple of 8 blocks keeps a block's tiles on one XCD)
+// slots: blocks that fit the card at once (a multiple of 8 keeps a block's tiles on one XCD)
 template <int BM, int BN, int WM, int WN, bool AK, bool BKM, int EPI, int ACT>
-hipError_t go(GemmArgs g, int per_cu, int cus, hipStream_t s)
+hipError_t go(GemmArgs g, int splits, int slots, hipStream_t s)
 {
-    const int64_t tiles = count_tiles<BM, BN, EPI>(g);
+    const int64_t total = (int64_t)((g.K + kBK - 1) / kBK) * g.nseg;
+    g.steps = (int)(((total + splits - 1) / splits + kBufs - 1) / kBufs * kBufs);
+    g.splits = (int)((total + g.steps - 1) / g.steps);
+    const int64_t tiles = count_tiles<BM, BN, EPI>(g) * g.splits;
     if (tiles > (int64_t)1 << 30) return hipErrorInvalidValue;
-    const int slots = per_cu * cus >= 8 ? per_cu * cus & ~7 : 8;
+    g.tiles = (int)tiles;
     const unsigned grid = (unsigned)(tiles < slots ? tiles : slots);
     hipLaunchKernelGGL((k_ffn_gemm<BM, BN, WM, WN, AK, BKM, EPI, ACT>), dim3(grid), dim3(64 * WM * WN), 0, s, g);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || g.splits == 1) return e;
+    size_t most = 0;
+    for (int i = 0; i < g.np; i++) most = most > (size_t)g.p[i].M * g.p[i].N ? most : (size_t)g.p[i].M * g.p[i].N;
+    const size_t blocks = (most / 8 + 255) / 256;
+    hipLaunchKernelGGL((k_ffn_join<EPI, ACT>), dim3((unsigned)(blocks < 2048 ? blocks : 2048), (unsigned)g.np), dim3(256), 0, s, g);
     return hipGetLastError();
 }
 
-template <bool AK, bool BKM, int EPI, int ACT = 0>
-hipError_t gemm(GemmArgs g, hipStream_t s)
+// Microseconds that a product is expected to take with BM x BN tiles and its reduction cut in `splits`.
+// From timings of the five products at 1 to 8192 tokens, widths 512 to 14336 (the choice is within 10 % of
+// the best tile and split of each): a step of 32 k on one CU takes 0.72 us for a 256 x 256 tile, 0.27 for
+// 128 x 128 (two blocks share a CU, 0.55 for both) and 0.145 for 64 x 64 (four blocks; 0.21 alone), so a
+// large tile does 1.5 and 3 times the work of the smaller ones in the same time, and wins where it fills
+// the card: 4096 tokens down 147 us against 223 and 381, but 1024 tokens d h 93 against 67 and 91.  What
+// comes back from a cut reduction crosses memory twice more in fp32 (6144 -> 3584 at 64 tokens: whole 41 us,
+// in eight parts 19).
+struct Shape {
+    int tile, resident;
+    double step, alone, tail;  // per step beside others, per step alone, per tile's end
+};
+constexpr Shape kShapes[3] = {{256, 1, 0.72, 0.54, 6.0}, {128, 2, 0.27, 0.24, 1.5}, {64, 4, 0.145, 0.21, 0.5}};
+
+double expected_us(const Shape &c, int64_t tiles, int64_t steps, int splits, int cus, double in_bytes, double out_bytes, double part_bytes)
 {
-    const int cus = compute_units();
-    if (count_tiles<256, 256, EPI>(g) >= 200) return go<256, 256, 2, 2, AK, BKM, EPI, ACT>(g, 1, cus, s);
-    if (count_tiles<128, 128, EPI>(g) >= 200) return go<128, 128, 2, 2, AK, BKM, EPI, ACT>(g, 2, cus, s);
-    return go<64, 64, 2, 1, AK, BKM, EPI, ACT>(g, 4, cus, s);
+    const int64_t per = ((steps + splits - 1) / splits + kBufs - 1) / kBufs * kBufs, parts = (steps + per - 1) / per;
+    const int64_t n = (tiles * parts + cus - 1) / cus;  // tiles of the busiest CU
+    const double one = c.step * n > c.alone ? c.step * n : c.alone;
+    double work = per * one + c.tail * n;
+    const double mem = in_bytes / 4.5e6;
+    if (mem > work) work = mem;
+    return 4.0 + work + out_bytes / 4.4e6 + (parts > 1 ? 4.0 + 2.0 * parts * part_bytes / 5e6 : 0.0);
+}
+
+template <bool AK, bool BKM, int EPI, int ACT = 0>
+hipError_t gemm(GemmArgs g, float *part, size_t part_floats, hipStream_t s)
+{
+    const int cus = compute_units() >= 8 ? compute_units() & ~7 : 8;
+    const int64_t steps = (int64_t)((g.K + kBK - 1) / kBK) * g.nseg;
+    size_t floats = 0;
+    double in = 0, out = 0;
+    for (int i = 0; i < g.np; i++) {
+        const double mn = (double)g.p[i].M * g.p[i].N, wide = EPI == EPI_GU ? 2 : 1;
+        floats += (size_t)g.p[i].M * g.p[i].N * (EPI == EPI_GU ? 2 : 1);
+        in += 2.0 * g.K * g.nseg * (g.p[i].M + wide * g.p[i].N);
+        out += EPI == EPI_STORE ? mn * (g.ct == DT_F32 ? 4 : 2)
+                                : EPI == EPI_GU ? mn * (2 * (g.h ? g.planes : 0) + (g.gu ? 8 : 0)) : mn * (8 + 2 * g.planes * ((g.h ? 1 : 0) + (g.dgu ? 2 : 0)));
+    }
+    const int64_t tiles[3] = {count_tiles<256, 256, EPI>(g), count_tiles<128, 128, EPI>(g), count_tiles<64, 64, EPI>(g)};
+    int cfg = 0, splits = 1;
+    double best = 1e30;
+    for (int c = 0; c < 3; c++)
+        for (int sp = 1; sp <= 16 && (sp == 1 || (steps / sp >= kBufs && floats * sp <= part_floats)); sp++) {
+            const double t = expected_us(kShapes[c], tiles[c], steps, sp, cus, in, out, 4.0 * floats);
+            if (t < best) best = t, cfg = c, splits = sp;
+        }
+    for (int i = 0; i < g.np; i++) {
+        g.p[i].part = part;
+        part += (size_t)splits * g.p[i].M * g.p[i].N * (EPI == EPI_GU ? 2 : 1);
+    }
+    if (cfg == 0) return go<256, 256, 2, 2, AK, BKM, EPI, ACT>(g, splits, cus, s);
+    if (cfg == 1) return go<128, 128, 2, 2, AK, BKM, EPI, ACT>(g, splits, 2 * cus, s);
+    return go<64, 64, 2, 1, AK, BKM, EPI, ACT>(g, splits, 4 * cus, s);
 }
 
 // Product i of g.
@@ -634,7 +768,7 @@ static hipError_t gate_up(const FfnArgs &a, uint16_t *h, int planes, float *gu, 
     g.nseg = 1, g.K = a.D;
     p.a[0] = a.x, p.b[0] = a.wg, g.b2 = a.wu;
     g.planes = planes, g.h = h, g.gu = gu;
-    return a.act == ACT_SITU ? gemm<false, false, EPI_GU, ACT_SITU>(g, s) : gemm<false, false, EPI_GU, ACT_SWIGLU>(g, s);
+    return a.act == ACT_SITU ? gemm<false, false, EPI_GU, ACT_SITU>(g, a.part, a.part_floats, s) : gemm<false, false, EPI_GU, ACT_SWIGLU>(g, a.part, a.part_floats, s);
 }
 
 hipError_t launch_ffn_forward(const FfnArgs &a, hipStream_t s)
@@ -646,7 +780,7 @@ hipError_t launch_ffn_forward(const FfnArgs &a, hipStream_t s)
     Prob &p = prob(g, a.T, a.D, a.I, a.I, a.y);
     g.nseg = planes, g.K = a.I, g.ct = a.yt, g.acc = a.acc;
     for (int k = 0; k < planes; k++) p.a[k] = a.h + (size_t)k * a.T * a.I, p.b[k] = a.wd;
-    return gemm<false, false, EPI_STORE>(g, s);
+    return gemm<false, false, EPI_STORE>(g, a.part, a.part_floats, s);
 }
 
 hipError_t launch_ffn_backward(const FfnArgs &a, hipStream_t s)
@@ -669,7 +803,7 @@ hipError_t launch_ffn_backward(const FfnArgs &a, hipStream_t s)
         g.planes = px > pw ? px : pw, g.gu = const_cast<float *>(gu);
         g.h = a.dwd ? a.h : nullptr;
         g.dgu = a.dx || dwgu ? a.dgu : nullptr;
-        e = a.act == ACT_SITU ? gemm<false, true, EPI_DGU, ACT_SITU>(g, s) : gemm<false, true, EPI_DGU, ACT_SWIGLU>(g, s);
+        e = a.act == ACT_SITU ? gemm<false, true, EPI_DGU, ACT_SITU>(g, a.part, a.part_floats, s) : gemm<false, true, EPI_DGU, ACT_SWIGLU>(g, a.part, a.part_floats, s);
         if (e != hipSuccess) return e;
     }
     if (a.dx) {
@@ -680,7 +814,7 @@ hipError_t launch_ffn_backward(const FfnArgs &a, hipStream_t s)
             p.a[2 * k] = a.dgu + k * T * 2 * I, p.b[2 * k] = a.wg;
             p.a[2 * k + 1] = a.dgu + k * T * 2 * I + I, p.b[2 * k + 1] = a.wu;
         }
-        if ((e = gemm<false, true, EPI_STORE>(g, s)) != hipSuccess) return e;
+        if ((e = gemm<false, true, EPI_STORE>(g, a.part, a.part_floats, s)) != hipSuccess) return e;
     }
     if (pw) {
         GemmArgs g{};
@@ -695,7 +829,7 @@ hipError_t launch_ffn_backward(const FfnArgs &a, hipStream_t s)
             Prob &p = prob(g, a.D, a.I, a.D, a.I, a.dwd);
             for (int k = 0; k < pw; k++) p.a[k] = a.dy, p.b[k] = a.h + k * T * I;
         }
-        return gemm<true, true, EPI_STORE>(g, s);
+        return gemm<true, true, EPI_STORE>(g, a.part, a.part_floats, s);
     }
     return hipSuccess;
 }
