@@ -107,6 +107,9 @@ struct FfnArgs {
     int dxt, dwt;
 };
 
+constexpr int kFewTokens = 64;  // most tokens of ffn_few.hip
+hipError_t launch_ffn_few_gate_up(const FfnArgs &a, uint16_t *h, int planes, float *gu, hipStream_t s);
+hipError_t launch_ffn_few_down(const FfnArgs &a, int planes, hipStream_t s);
 hipError_t launch_ffn_forward(const FfnArgs &a, hipStream_t s);
 hipError_t launch_ffn_backward(const FfnArgs &a, hipStream_t s);
 

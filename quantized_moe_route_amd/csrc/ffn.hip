@@ -20,6 +20,7 @@
 
 #include "block_internal.h"
 #include "common.h"
+#include "ffn_act.h"
 
 namespace moe {
 
@@ -170,53 +171,6 @@ struct Tile {
         }
     }
 };
-
-// Reciprocal to 1 ulp (v_rcp_f32): the correctly rounded division takes ten instructions, and an
-// epilogue's exponentials and divisions stand between two tiles of matrix work.
-__device__ __forceinline__ float rcp(float z) { return __builtin_amdgcn_rcpf(z); }
-
-__device__ __forceinline__ float sigm(float z) { return rcp(1.f + __expf(-z)); }
-
-// tanh z = sign(z) (1 - e) / (1 + e), e = exp(-2 |z|); below 1/8, where 1 - e cancels, the odd series
-// to z^7 (its next term is below 2^-29 of z there).
-__device__ __forceinline__ float tanh_(float z)
-{
-    const float e = __expf(-2.f * fabsf(z)), z2 = z * z;
-    const float s = z * (1.f + z2 * (-1.f / 3.f + z2 * (2.f / 15.f + z2 * (-17.f / 315.f))));
-    return z2 < 1.f / 64.f ? s : copysignf((1.f - e) * rcp(1.f + e), z);
-}
-
-// The layer's activations (moe_act): h and its two derivatives.
-template <int ACT>
-__device__ __forceinline__ float gated(float g, float u)
-{
-    if constexpr (ACT == ACT_SITU) return 4.f * tanh_(0.25f * g) * sigm(g) * (25.f * tanh_(u * (1.f / 25.f)));
-    return g * sigm(g) * u;
-}
-
-__device__ __forceinline__ float sech2(float z)
-{
-    const float e = __expf(-2.f * fabsf(z)), r = rcp(1.f + e);
-    return 4.f * e * r * r;
-}
-
-template <int ACT>
-__device__ __forceinline__ void gated_grad(float g, float u, float &h, float &dhdg, float &dhdu)
-{
-    const float s = sigm(g);
-    if constexpr (ACT == ACT_SITU) {
-        const float zg = 0.25f * g, zu = u * (1.f / 25.f);
-        const float A = 4.f * tanh_(zg) * s, B = 25.f * tanh_(zu);
-        h = A * B;
-        dhdg = (sech2(zg) * s + A * (1.f - s)) * B;
-        dhdu = A * sech2(zu);
-        return;
-    }
-    const float silu = g * s;
-    h = silu * u;
-    dhdg = u * (s + silu * (1.f - s));
-    dhdu = silu;
-}
 
 // Eight consecutive values as `planes` bf16 rows, plane p at dst + p * stride: one rounding, or the
 // three terms whose sum is the value (a value that is not finite stays in the first term).
@@ -613,12 +567,13 @@ __global__ __launch_bounds__(64 * WM *WN, 1) void k_ffn_gemm(GemmArgs g)
     }
 }
 
-// Compute units of the current device.
+// Compute units of the current device, down to a multiple of 8 (a grid of such a multiple keeps a block's
+// tiles on one XCD).
 int compute_units()
 {
     int dev = 0, n = 0;
     if (hipGetDevice(&dev) != hipSuccess || hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0) return 256;
-    return n;
+    return n >= 8 ? n & ~7 : 8;
 }
 
 // Joins the parts of product blockIdx.y in order, eight columns a thread, and finishes it.
@@ -673,7 +628,7 @@ int64_t count_tiles(GemmArgs &g)
     return n;
 }
 
-// slots: blocks that fit the card at once (a multiple of 8 keeps a block's tiles on one XCD)
+// slots: blocks that fit the card at once
 template <int BM, int BN, int WM, int WN, bool AK, bool BKM, int EPI, int ACT>
 hipError_t go(GemmArgs g, int splits, int slots, hipStream_t s)
 {
@@ -701,53 +656,72 @@ hipError_t go(GemmArgs g, int splits, int slots, hipStream_t s)
 // large tile does 1.5 and 3 times the work of the smaller ones in the same time, and wins where it fills
 // the card: 4096 tokens down 147 us against 223 and 381, but 1024 tokens d h 93 against 67 and 91.  What
 // comes back from a cut reduction crosses memory twice more in fp32 (6144 -> 3584 at 64 tokens: whole 41 us,
-// in eight parts 19).
+// in eight parts 19).  Memory brings what the resident blocks have asked for, three steps each, in about a
+// microsecond.
 struct Shape {
     int tile, resident;
-    double step, alone, tail;  // per step beside others, per step alone, per tile's end
+    double step, alone, tail;  // us per step beside others, per step alone, per tile's end
 };
 constexpr Shape kShapes[3] = {{256, 1, 0.72, 0.54, 6.0}, {128, 2, 0.27, 0.24, 1.5}, {64, 4, 0.145, 0.21, 0.5}};
 
-double expected_us(const Shape &c, int64_t tiles, int64_t steps, int splits, int cus, double in_bytes, double out_bytes, double part_bytes)
+double expected_us(const Shape &c, int64_t tiles, int64_t steps, int splits, int cus, int rows, double in_bytes, double out_bytes,
+                   double part_bytes)
 {
     const int64_t per = ((steps + splits - 1) / splits + kBufs - 1) / kBufs * kBufs, parts = (steps + per - 1) / per;
-    const int64_t n = (tiles * parts + cus - 1) / cus;  // tiles of the busiest CU
+    const int64_t blocks = tiles * parts, n = (blocks + cus - 1) / cus;  // n: tiles of the busiest CU
     const double one = c.step * n > c.alone ? c.step * n : c.alone;
     double work = per * one + c.tail * n;
-    const double mem = in_bytes / 4.5e6;
+    const int64_t resident = blocks < (int64_t)c.resident * cus ? blocks : (int64_t)c.resident * cus;
+    const double asked = (double)resident * (kBufs - 1) * kBK * 2 * (c.tile + (rows < c.tile ? rows : c.tile));
+    const double mem = in_bytes / (asked < 4.5e6 ? asked : 4.5e6);
     if (mem > work) work = mem;
     return 4.0 + work + out_bytes / 4.4e6 + (parts > 1 ? 4.0 + 2.0 * parts * part_bytes / 5e6 : 0.0);
+}
+
+struct Plan {
+    int shape = 0, splits = 1;
+    double us = 1e30;
+};
+
+template <int EPI>
+Plan plan(GemmArgs &g, size_t part_floats)
+{
+    const int cus = compute_units();
+    const int64_t steps = (int64_t)((g.K + kBK - 1) / kBK) * g.nseg;
+    size_t floats = 0;
+    double in = 0, out = 0;
+    int rows = 0;
+    for (int i = 0; i < g.np; i++) {
+        const Prob &p = g.p[i];
+        const double mn = (double)p.M * p.N, wide = EPI == EPI_GU ? 2 : 1;
+        floats += (size_t)p.M * p.N * (EPI == EPI_GU ? 2 : 1);
+        in += 2.0 * g.K * g.nseg * (p.M + wide * p.N);
+        out += EPI == EPI_STORE ? mn * (g.ct == DT_F32 ? 4 : 2)
+                                : EPI == EPI_GU ? mn * (2 * (g.h ? g.planes : 0) + (g.gu ? 8 : 0)) : mn * (8 + 2 * g.planes * ((g.h ? 1 : 0) + (g.dgu ? 2 : 0)));
+        rows = rows > p.M ? rows : p.M;
+    }
+    const int64_t tiles[3] = {count_tiles<256, 256, EPI>(g), count_tiles<128, 128, EPI>(g), count_tiles<64, 64, EPI>(g)};
+    Plan best;
+    for (int c = 0; c < 3; c++)
+        for (int sp = 1; sp <= 16 && (sp == 1 || (steps / sp >= kBufs && floats * sp <= part_floats)); sp++) {
+            const double t = expected_us(kShapes[c], tiles[c], steps, sp, cus, rows, in, out, 4.0 * floats);
+            if (t < best.us) best = {c, sp, t};
+        }
+    return best;
 }
 
 template <bool AK, bool BKM, int EPI, int ACT = 0>
 hipError_t gemm(GemmArgs g, float *part, size_t part_floats, hipStream_t s)
 {
-    const int cus = compute_units() >= 8 ? compute_units() & ~7 : 8;
-    const int64_t steps = (int64_t)((g.K + kBK - 1) / kBK) * g.nseg;
-    size_t floats = 0;
-    double in = 0, out = 0;
-    for (int i = 0; i < g.np; i++) {
-        const double mn = (double)g.p[i].M * g.p[i].N, wide = EPI == EPI_GU ? 2 : 1;
-        floats += (size_t)g.p[i].M * g.p[i].N * (EPI == EPI_GU ? 2 : 1);
-        in += 2.0 * g.K * g.nseg * (g.p[i].M + wide * g.p[i].N);
-        out += EPI == EPI_STORE ? mn * (g.ct == DT_F32 ? 4 : 2)
-                                : EPI == EPI_GU ? mn * (2 * (g.h ? g.planes : 0) + (g.gu ? 8 : 0)) : mn * (8 + 2 * g.planes * ((g.h ? 1 : 0) + (g.dgu ? 2 : 0)));
-    }
-    const int64_t tiles[3] = {count_tiles<256, 256, EPI>(g), count_tiles<128, 128, EPI>(g), count_tiles<64, 64, EPI>(g)};
-    int cfg = 0, splits = 1;
-    double best = 1e30;
-    for (int c = 0; c < 3; c++)
-        for (int sp = 1; sp <= 16 && (sp == 1 || (steps / sp >= kBufs && floats * sp <= part_floats)); sp++) {
-            const double t = expected_us(kShapes[c], tiles[c], steps, sp, cus, in, out, 4.0 * floats);
-            if (t < best) best = t, cfg = c, splits = sp;
-        }
+    const int cus = compute_units();
+    const Plan c = plan<EPI>(g, part_floats);
     for (int i = 0; i < g.np; i++) {
         g.p[i].part = part;
-        part += (size_t)splits * g.p[i].M * g.p[i].N * (EPI == EPI_GU ? 2 : 1);
+        part += (size_t)c.splits * g.p[i].M * g.p[i].N * (EPI == EPI_GU ? 2 : 1);
     }
-    if (cfg == 0) return go<256, 256, 2, 2, AK, BKM, EPI, ACT>(g, splits, cus, s);
-    if (cfg == 1) return go<128, 128, 2, 2, AK, BKM, EPI, ACT>(g, splits, 2 * cus, s);
-    return go<64, 64, 2, 1, AK, BKM, EPI, ACT>(g, splits, 4 * cus, s);
+    if (c.shape == 0) return go<256, 256, 2, 2, AK, BKM, EPI, ACT>(g, c.splits, cus, s);
+    if (c.shape == 1) return go<128, 128, 2, 2, AK, BKM, EPI, ACT>(g, c.splits, 2 * cus, s);
+    return go<64, 64, 2, 1, AK, BKM, EPI, ACT>(g, c.splits, 4 * cus, s);
 }
 
 // Product i of g.
@@ -760,6 +734,16 @@ Prob &prob(GemmArgs &g, int M, int N, int lda, int ldb, void *c)
 
 }  // namespace
 
+// What the few-token kernels of ffn_few.hip are expected to take: the weights at 5.6 TB/s, and the tokens,
+// which every block reads, from the caches.  At 3584 -> 6144 -> 3584 the two kernels take 18 and 11 us for one
+// token (the tiled products 29 and 19) and 46 and 35 for 64 (39 and 23).
+static double few_us(int T, int N, int K, int planes, bool pair)
+{
+    const int tiles = T <= 16 ? 1 : T <= 32 ? 2 : 4, cols = pair ? (tiles == 1 ? 8 : 16) : 16;
+    const double weights = 2.0 * (pair ? 2 : 1) * N * K, tokens = (double)((N + cols - 1) / cols) * T * K * 2.0 * planes;
+    return 3.0 + weights / 5.6e6 + tokens / (tiles == 1 ? 10e6 : 7e6);
+}
+
 // g and u (kept in gu unless null), h in `planes` terms unless null
 static hipError_t gate_up(const FfnArgs &a, uint16_t *h, int planes, float *gu, hipStream_t s)
 {
@@ -768,7 +752,9 @@ static hipError_t gate_up(const FfnArgs &a, uint16_t *h, int planes, float *gu, 
     g.nseg = 1, g.K = a.D;
     p.a[0] = a.x, p.b[0] = a.wg, g.b2 = a.wu;
     g.planes = planes, g.h = h, g.gu = gu;
-    return a.act == ACT_SITU ? gemm<false, false, EPI_GU, ACT_SITU>(g, a.part, a.part_floats, s) : gemm<false, false, EPI_GU, ACT_SWIGLU>(g, a.part, a.part_floats, s);
+    if (a.T <= kFewTokens && few_us(a.T, a.I, a.D, 1, true) < plan<EPI_GU>(g, a.part_floats).us) return launch_ffn_few_gate_up(a, h, planes, gu, s);
+    return a.act == ACT_SITU ? gemm<false, false, EPI_GU, ACT_SITU>(g, a.part, a.part_floats, s)
+                             : gemm<false, false, EPI_GU, ACT_SWIGLU>(g, a.part, a.part_floats, s);
 }
 
 hipError_t launch_ffn_forward(const FfnArgs &a, hipStream_t s)
@@ -780,6 +766,7 @@ hipError_t launch_ffn_forward(const FfnArgs &a, hipStream_t s)
     Prob &p = prob(g, a.T, a.D, a.I, a.I, a.y);
     g.nseg = planes, g.K = a.I, g.ct = a.yt, g.acc = a.acc;
     for (int k = 0; k < planes; k++) p.a[k] = a.h + (size_t)k * a.T * a.I, p.b[k] = a.wd;
+    if (a.T <= kFewTokens && few_us(a.T, a.D, a.I, planes, false) < plan<EPI_STORE>(g, a.part_floats).us) return launch_ffn_few_down(a, planes, s);
     return gemm<false, false, EPI_STORE>(g, a.part, a.part_floats, s);
 }
 
