@@ -44,6 +44,7 @@ class _Handle:
         torch = _torch()
         L = C.lib()
         self.device, self.desc = device, desc
+        self._index = device.index
         n = ctypes.c_size_t()
         C.check(getattr(L, size_fn)(ctypes.byref(desc), ctypes.byref(n)), size_fn)
         self.workspace_bytes = n.value
@@ -59,23 +60,28 @@ class _Handle:
         torch = _torch()
         if self._h is None:
             raise RuntimeError(f"{fn}: the handle is closed")
-        with torch.cuda.device(self.device):
-            s = torch.cuda.current_stream(self.device)
-            if s.cuda_stream != self._home and not torch.cuda.is_current_stream_capturing():
-                self.workspace.record_stream(s)  # not reused for others while this stream works in it
-            C.check(getattr(C.lib(), fn)(self._h, *args, s.cuda_stream), fn)
+        if torch.cuda.current_device() != self._index:
+            with torch.cuda.device(self._index):
+                return self._call(fn, *args)
+        stream = torch._C._cuda_getCurrentRawStream(self._index)
+        if stream != self._home and not torch.cuda.is_current_stream_capturing():
+            # not reused for others while this stream works in it
+            self.workspace.record_stream(torch.cuda.current_stream(self._index))
+        status = getattr(C.lib(), fn)(self._h, *args, stream)
+        if status:
+            C.check(status, fn)
 
     def _take(self, t, what: str, shape, *dtypes):
         """Checks one tensor argument and returns it."""
+        if t.shape == shape and t.dtype in dtypes and t.device == self.device and t.is_contiguous():
+            return t
         if t.device != self.device:
             raise ValueError(f"{what} is on {t.device}, the operator on {self.device}")
-        if tuple(t.shape) != tuple(shape):
+        if t.shape != shape:
             raise ValueError(f"{what} has shape {tuple(t.shape)}, not {tuple(shape)}")
         if t.dtype not in dtypes:
             raise TypeError(f"{what} has dtype {t.dtype}, not {' or '.join(str(d) for d in dtypes)}")
-        if not t.is_contiguous():
-            raise ValueError(f"{what} is not contiguous")
-        return t
+        raise ValueError(f"{what} is not contiguous")
 
     def _new(self, shape, dtype):
         return _torch().empty(shape, dtype=dtype, device=self.device)

@@ -113,12 +113,33 @@ __device__ __forceinline__ uint32_t encode4(const float (&f)[4], float &scale)
         scale = 0.f;
         return 0u;
     }
-    // |f / scale| <= 448 (1 + 2^-22): rounds to at most the largest code, nothing to clamp
-    int lo = __builtin_amdgcn_cvt_pk_fp8_f32(f[0] / scale, f[1] / scale, 0, false);
-    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f[2] / scale, f[3] / scale, lo, true);
+    // |f| / scale <= 448 (1 + 2^-22): rounds to at most the largest code, nothing to clamp.  One division a
+    // run: with one an element the step was bound by its arithmetic (44 M parameters 170 us).
+    const float inv = 1.f / scale;
+    int lo = __builtin_amdgcn_cvt_pk_fp8_f32(f[0] * inv, f[1] * inv, 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f[2] * inv, f[3] * inv, lo, true);
 }
 
-__device__ __forceinline__ double pow_steps(double beta, unsigned long long t) { return pow(beta, (double)t); }
+// beta^t by squaring: one thread of one block waits for it, and pow() takes a microsecond.
+__device__ double power(double beta, unsigned long long t)
+{
+    double r = 1.0;
+    for (; t; t >>= 1, beta *= beta)
+        if (t & 1) r *= beta;
+    return r;
+}
+
+// Starts a step: counts it and puts its numbers where every block finds them.
+__device__ void begin_step(const AdamArgs &a, float clip)
+{
+    const unsigned long long t = a.ctl->step + 1;
+    const double lr = a.lr_dev ? (double)*a.lr_dev : a.lr;
+    a.ctl->step = t;
+    a.ctl->clip = clip;
+    a.ctl->lr = (float)lr;
+    a.ctl->lr_m = (float)(lr / (1.0 - power(a.beta1, t)));
+    a.ctl->root_v = (float)(1.0 / sqrt(1.0 - power(a.beta2, t)));
+}
 
 }  // namespace
 
@@ -148,86 +169,77 @@ __global__ __launch_bounds__(256) void k_adam_map(const AdamTensor *__restrict__
 __global__ void k_adam_set_step(AdamCtl *ctl, unsigned long long step)
 {
     ctl->step = step;
-    ctl->ticket = 0;
-    ctl->clip = 1.f;
-    ctl->norm = 0.f;
 }
 
-// Sum of squares of the gradients: a block adds its chunks' squares (fp32 within a lane's run of
-// four, fp64 beyond), the last block to finish adds the blocks' sums in order and sets the clip
-// factor and the step count.
+// Sums of squares of the gradients, one fp64 number a block: fp32 within a lane's sixteen elements of a
+// chunk, fp64 beyond.
 __global__ __launch_bounds__(256) void k_adam_norm(AdamArgs a)
 {
     __shared__ double s[4];
-    __shared__ bool last;
     const int tid = threadIdx.x;
     double sum = 0.0;
     for (int64_t c = blockIdx.x; c < a.chunks; c += gridDim.x) {
         const AdamTensor &t = a.tab[a.chunk_of[c]];
-        const int64_t e0 = chunk_elem0(t, c, a.chunk_elems);
-        for (int k = 4 * tid; k < a.chunk_elems; k += 1024) {
-            const int64_t i = e0 + k;
-            if (i >= t.n) break;
-            float g[4];
-            ld4(t.g, t.gt, t.vec, i, t.n - i, g);
-            double q = 0.0;
+        const int64_t e0 = chunk_elem0(t, c, a.chunk_elems), n = t.n;
+        const void *const p = t.g;
+        const int gt = t.gt;
+        float q = 0.f;
+        if (t.vec && gt == DT_F32 && e0 + a.chunk_elems <= n) {
+            // a whole chunk: every load requested before the first is used
+            const f32x4 *const v = (const f32x4 *)((const float *)p + e0) + tid;
+            f32x4 g[4];
 #pragma unroll
-            for (int e = 0; e < 4; e++) q += (double)g[e] * (double)g[e];
-            sum += q;
+            for (int k = 0; k < 4; k++) g[k] = v[1024 * k < a.chunk_elems ? 256 * k : 0];
+#pragma unroll
+            for (int k = 0; k < 4; k++)
+                if (1024 * k < a.chunk_elems) q += (g[k][0] * g[k][0] + g[k][1] * g[k][1]) + (g[k][2] * g[k][2] + g[k][3] * g[k][3]);
+        } else {
+            for (int k = 4 * tid; k < a.chunk_elems && e0 + k < n; k += 1024) {
+                float g[4];
+                ld4(p, gt, t.vec, e0 + k, n - e0 - k, g);
+                q += (g[0] * g[0] + g[1] * g[1]) + (g[2] * g[2] + g[3] * g[3]);
+            }
         }
+        sum += (double)q;
     }
     sum = wave_sum_f64(sum);
     if ((tid & 63) == 0) s[tid >> 6] = sum;
     __syncthreads();
-    if (tid == 0) {
-        __hip_atomic_store(a.part + blockIdx.x, (s[0] + s[1]) + (s[2] + s[3]), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        __threadfence();
-        last = atomicAdd(&a.ctl->ticket, 1u) == gridDim.x - 1;
-    }
-    __syncthreads();
-    if (!last) return;
-    __threadfence();
-    sum = 0.0;
-    for (int b = tid; b < (int)gridDim.x; b += 256) sum += __hip_atomic_load(a.part + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    sum = wave_sum_f64(sum);
-    __syncthreads();
-    if ((tid & 63) == 0) s[tid >> 6] = sum;
-    __syncthreads();
-    if (tid == 0) {
-        const double norm = sqrt((s[0] + s[1]) + (s[2] + s[3]));
-        const bool ok = isfinite(norm);
-        a.ctl->norm = (float)norm;
-        a.ctl->clip = ok ? (float)((double)a.max_norm / fmax(norm, (double)a.max_norm)) : -1.f;
-        if (ok) a.ctl->step += 1;
-        a.ctl->ticket = 0;
-        if (a.norm_out) *a.norm_out = (float)norm;
-    }
+    if (tid == 0) a.part[blockIdx.x] = (s[0] + s[1]) + (s[2] + s[3]);
 }
 
-// The step count of a set without elements.
-__global__ void k_adam_bump(AdamCtl *ctl) { ctl->step += 1; }
+// Begins the step; with clipping, from the nb blocks' sums added in order.  (A launch of its own: a last
+// block found by a counter waits for hundreds of draws from it.)
+__global__ __launch_bounds__(256) void k_adam_begin(AdamArgs a, int nb)
+{
+    __shared__ double s[4];
+    const int tid = threadIdx.x;
+    double sum = 0.0;
+    for (int b = tid; b < nb; b += 256) sum += a.part[b];
+    sum = wave_sum_f64(sum);
+    if ((tid & 63) == 0) s[tid >> 6] = sum;
+    __syncthreads();
+    if (tid != 0) return;
+    if (!a.clipped) return begin_step(a, 1.f);
+    const double norm = sqrt((s[0] + s[1]) + (s[2] + s[3]));
+    if (isfinite(norm))
+        begin_step(a, (float)((double)a.max_norm / fmax(norm, (double)a.max_norm)));
+    else
+        a.ctl->clip = -1.f;  // the step is skipped
+    if (a.norm_out) *a.norm_out = (float)norm;
+}
 
 // One chunk per block.
 template <bool E4M3>
 __global__ __launch_bounds__(256) void k_adam_step(AdamArgs a)
 {
-    __shared__ float cf[3];
     const int tid = threadIdx.x, lane = tid & 63;
-    const float clip = a.clipped ? a.ctl->clip : 1.f;
+    const float clip = a.ctl->clip;
     if (clip < 0.f) return;  // a gradient norm that is not finite: nothing changes
-    if (tid == 0) {
-        // every block reads the count before it takes its ticket, and the last ticket raises it
-        const unsigned long long n = a.clipped ? a.ctl->step : a.ctl->step + 1;
-        const double lr = a.lr_dev ? (double)*a.lr_dev : a.lr;
-        cf[0] = (float)lr;
-        cf[1] = (float)(lr / (1.0 - pow_steps(a.beta1, n)));
-        cf[2] = (float)sqrt(1.0 - pow_steps(a.beta2, n));
-    }
-    __syncthreads();
     const int64_t c = blockIdx.x;
     const AdamTensor t = a.tab[a.chunk_of[c]];
     const float b1 = (float)a.beta1, b1c = (float)(1.0 - a.beta1), b2 = (float)a.beta2, b2c = (float)(1.0 - a.beta2);
-    const float decay = (float)(1.0 - (double)cf[0] * t.lr_scale * t.wd), lr = cf[1] * t.lr_scale, root2 = cf[2];
+    const float decay = (float)(1.0 - (double)a.ctl->lr * t.lr_scale * t.wd), lr = a.ctl->lr_m * t.lr_scale, iroot2 = a.ctl->root_v;
     const int64_t e0 = chunk_elem0(t, c, a.chunk_elems);
     void *const pp = t.master ? (void *)t.master : t.p;
     const int pt = t.master ? DT_F32 : t.pt;
@@ -253,7 +265,8 @@ __global__ __launch_bounds__(256) void k_adam_step(AdamArgs a)
             m[e] = m[e] * b1 + gc * b1c;
             v[e] = v[e] * b2 + gc * gc * b2c;
             root[e] = sqrtf(v[e]);
-            p[e] = p[e] * decay - lr * (m[e] / (root[e] / root2 + a.eps));
+            // v_rcp_f32 is within 1 ulp: of the update, not of the parameter
+            p[e] = p[e] * decay - lr * (m[e] * __builtin_amdgcn_rcpf(root[e] * iroot2 + a.eps));
         }
         st4(pp, pt, t.vec, i, left, p);
         if (t.master) st4(t.p, t.pt, t.vec, i, left, p);
@@ -272,10 +285,6 @@ __global__ __launch_bounds__(256) void k_adam_step(AdamArgs a)
             st4(t.m, DT_F32, t.vec, i, left, m);
             st4(t.v, DT_F32, t.vec, i, left, v);
         }
-    }
-    if (!a.clipped && tid == 0 && atomicAdd(&a.ctl->ticket, 1u) == gridDim.x - 1) {
-        a.ctl->ticket = 0;
-        a.ctl->step += 1;
     }
 }
 
@@ -307,17 +316,11 @@ hipError_t launch_adam_set_step(AdamCtl *ctl, unsigned long long step, hipStream
 
 hipError_t launch_adam_step(const AdamArgs &a, hipStream_t s)
 {
-    if (a.clipped) {
-        const unsigned nb = (unsigned)(a.chunks < 1 ? 1 : a.chunks < kAdamNormBlocks ? a.chunks : kAdamNormBlocks);
-        hipLaunchKernelGGL(k_adam_norm, dim3(nb), dim3(256), 0, s, a);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
-    if (a.chunks == 0) {
-        if (a.clipped) return hipSuccess;
-        hipLaunchKernelGGL(k_adam_bump, dim3(1), dim3(1), 0, s, a.ctl);
-        return hipGetLastError();
-    }
+    const int nb = !a.clipped ? 0 : a.chunks < kAdamNormBlocks ? (int)a.chunks : kAdamNormBlocks;
+    if (nb > 0) hipLaunchKernelGGL(k_adam_norm, dim3((unsigned)nb), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(k_adam_begin, dim3(1), dim3(256), 0, s, a, nb);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.chunks == 0) return e;
     if (a.e4m3)
         hipLaunchKernelGGL((k_adam_step<true>), dim3((unsigned)a.chunks), dim3(256), 0, s, a);
     else

@@ -49,11 +49,11 @@ struct AdamTensor {
 };
 static_assert(sizeof(AdamTensor) == 80, "table layout");
 
-struct AdamCtl {              // in the workspace, zeroed by set_step
+struct AdamCtl {              // in the workspace, started by set_step
     unsigned long long step;  // steps taken
-    uint32_t ticket, pad;
-    float clip;               // of this step; < 0: the step is skipped
-    float norm;
+    // of the present step
+    float clip;               // < 0: the step is skipped
+    float lr, lr_m, root_v;   // lr, lr / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
 };
 
 struct AdamArgs {
@@ -70,7 +70,7 @@ struct AdamArgs {
     float *norm_out;
 };
 
-constexpr int kAdamNormBlocks = 1024;
+constexpr int kAdamNormBlocks = 2048;
 constexpr int kAdamPut = 40;  // table entries per upload launch (3.2 KB of arguments)
 
 struct AdamPut {
