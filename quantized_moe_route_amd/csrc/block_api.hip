@@ -136,7 +136,7 @@ moe_status check_norm_desc(const moe_norm_desc *d)
 size_t norm_bytes(const moe_norm_desc &d)
 {
     if (!(d.flags & MOE_NORM_BACKWARD)) return 0;
-    return up256((size_t)std::min(d.max_tokens, moe::kNormBlocks) * 3 * d.width * 4);
+    return up256((size_t)std::min(d.max_tokens, moe::norm_parts(d.width)) * 3 * d.width * 4);
 }
 
 // ---------------------------------------------------------------- AdamW

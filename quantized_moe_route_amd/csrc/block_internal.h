@@ -23,11 +23,14 @@ struct NormArgs {
     // backward (r_out and rstd are read)
     const void *dr_out, *dx;
     void *dr, *dy, *dg, *dw_post, *dw_next;
-    float *part;  // [kNormBlocks][3][D]
+    float *part;  // [norm_parts(D)][3][D]
 };
 
 constexpr int kMaxNormWidth = 16384;
-constexpr int kNormBlocks = 512;  // blocks of the backward, each with its own partial column sums
+constexpr int kWaveWidth = 512;  // widest row of a single wave
+
+// rows of partial column sums in the backward: its blocks, or its waves where each has a row
+constexpr int norm_parts(int width) { return width <= kWaveWidth ? 4096 : 512; }
 
 hipError_t launch_norm_forward(const NormArgs &a, hipStream_t s);
 hipError_t launch_norm_backward(const NormArgs &a, hipStream_t s);

@@ -20,25 +20,26 @@ namespace moe {
 
 namespace {
 
-template <int VEC>
-__device__ __forceinline__ void ld_vec(const void *p, int dt, size_t i, float (&f)[VEC])
+constexpr int kWaveRows = 8;  // rows of a block whose waves have a row each
+
+// Sixteen bytes at an element's own alignment: where the width or a pointer is not a multiple of 16 bytes
+// (TAIL), rows begin anywhere.
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+
+template <bool TAIL>
+__device__ __forceinline__ u32x4 ld16(const void *p)
 {
-    if constexpr (VEC == 8) {
-        if (dt == DT_F32) {
-            const f32x4 a = *(const f32x4 *)((const float *)p + i), b = *(const f32x4 *)((const float *)p + i + 4);
-#pragma unroll
-            for (int e = 0; e < 4; e++) f[e] = a[e], f[4 + e] = b[e];
-        } else {
-            const u32x4 v = *(const u32x4 *)((const uint16_t *)p + i);
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-                f[2 * e] = __uint_as_float(v[e] << 16);
-                f[2 * e + 1] = __uint_as_float(v[e] & 0xFFFF0000u);
-            }
-        }
-    } else {
-        f[0] = dt == DT_F32 ? ((const float *)p)[i] : bf16_bits_to_f32(((const uint16_t *)p)[i]);
-    }
+    if constexpr (TAIL) return *(const u32x4_any *)p;
+    return *(const u32x4 *)p;
+}
+
+template <bool TAIL>
+__device__ __forceinline__ void st16(void *p, u32x4 v)
+{
+    if constexpr (TAIL)
+        *(u32x4_any *)p = v;
+    else
+        *(u32x4 *)p = v;
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b)
@@ -47,40 +48,98 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b)
     return __builtin_bit_cast(uint32_t, v);
 }
 
-template <int VEC>
-__device__ __forceinline__ void st_vec(void *p, int dt, size_t i, const float (&f)[VEC])
-{
-    if constexpr (VEC == 8) {
-        if (dt == DT_F32) {
-            *(f32x4 *)((float *)p + i) = f32x4{f[0], f[1], f[2], f[3]};
-            *(f32x4 *)((float *)p + i + 4) = f32x4{f[4], f[5], f[6], f[7]};
-        } else {
-            *(u32x4 *)((uint16_t *)p + i) = u32x4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])};
+// Eight elements as they lie in memory; with TAIL only the first n < 8 of a row's last group may exist.
+template <int DT, bool TAIL>
+struct Raw {
+    static constexpr int kWords = DT == DT_F32 ? 8 : 4;
+    uint32_t w[kWords];
+
+    __device__ __forceinline__ void load(const void *p, size_t i, int n)
+    {
+        const char *q = (const char *)p + i * (DT == DT_F32 ? 4 : 2);
+        if (!TAIL || n >= 8) {
+#pragma unroll
+            for (int k = 0; k < kWords / 4; k++) {
+                const u32x4 v = ld16<TAIL>(q + 16 * k);
+#pragma unroll
+                for (int e = 0; e < 4; e++) w[4 * k + e] = v[e];
+            }
+            return;
         }
+#pragma unroll
+        for (int k = 0; k < kWords; k++) w[k] = 0u;
+#pragma unroll
+        for (int e = 0; e < 7; e++) {
+            if (e >= n) break;
+            if constexpr (DT == DT_F32)
+                w[e] = ((const uint32_t *)q)[e];
+            else
+                w[e >> 1] |= (uint32_t)((const uint16_t *)q)[e] << (16 * (e & 1));
+        }
+    }
+
+    __device__ __forceinline__ float at(int e) const
+    {
+        if constexpr (DT == DT_F32) return __uint_as_float(w[e]);
+        return __uint_as_float(e & 1 ? w[e >> 1] & 0xFFFF0000u : w[e >> 1] << 16);
+    }
+};
+
+template <bool TAIL>
+__device__ __forceinline__ void ld_vec(const void *p, int dt, size_t i, int n, float (&f)[8])
+{
+    if (dt == DT_F32) {
+        Raw<DT_F32, TAIL> r;
+        r.load(p, i, n);
+#pragma unroll
+        for (int e = 0; e < 8; e++) f[e] = r.at(e);
     } else {
+        Raw<DT_BF16, TAIL> r;
+        r.load(p, i, n);
+#pragma unroll
+        for (int e = 0; e < 8; e++) f[e] = r.at(e);
+    }
+}
+
+template <bool TAIL>
+__device__ __forceinline__ void st_vec(void *p, int dt, size_t i, int n, const float (&f)[8])
+{
+    char *q = (char *)p + i * (dt == DT_F32 ? 4 : 2);
+    if (!TAIL || n >= 8) {
+        if (dt == DT_F32) {
+            st16<TAIL>(q, __builtin_bit_cast(u32x4, f32x4{f[0], f[1], f[2], f[3]}));
+            st16<TAIL>(q + 16, __builtin_bit_cast(u32x4, f32x4{f[4], f[5], f[6], f[7]}));
+        } else {
+            st16<TAIL>(q, u32x4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])});
+        }
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 7; e++) {
+        if (e >= n) break;
         if (dt == DT_F32)
-            ((float *)p)[i] = f[0];
+            ((float *)q)[e] = f[e];
         else
-            ((uint16_t *)p)[i] = (uint16_t)pack_bf16(f[0], 0.f);
+            ((uint16_t *)q)[e] = (uint16_t)pack_bf16(f[e], 0.f);
     }
 }
 
 // The value that storing f as dt keeps.
-template <int VEC>
-__device__ __forceinline__ void round_to(int dt, float (&f)[VEC])
+__device__ __forceinline__ void round_to(int dt, float (&f)[8])
 {
     if (dt == DT_F32) return;
 #pragma unroll
-    for (int e = 0; e < VEC; e++) f[e] = (float)(__bf16)f[e];
+    for (int e = 0; e < 8; e++) f[e] = (float)(__bf16)f[e];
 }
 
-// Sum over the block (up to 16 waves).  scr: two rows of 16 floats used in turn, so one barrier
-// per sum is enough.
-__device__ __forceinline__ float block_sum(float v, float (*scr)[16], int &turn)
+// Sum over the threads of a row: a wave (WAVE), or the block of up to 16 waves.  scr: two rows of 16
+// floats used in turn, so one barrier per sum is enough.
+template <bool WAVE>
+__device__ __forceinline__ float row_sum(float v, float (*scr)[16], int &turn)
 {
     const int wv = threadIdx.x >> 6, nw = (blockDim.x + 63) >> 6;
     v = wave_sum_f32(v);
-    if (nw == 1) return v;
+    if (WAVE || nw == 1) return v;
     float *s = scr[turn];
     turn ^= 1;
     if ((threadIdx.x & 63) == 0) s[wv] = v;
@@ -90,66 +149,75 @@ __device__ __forceinline__ float block_sum(float v, float (*scr)[16], int &turn)
     return t;
 }
 
-// Elements of thread tid: NV groups of VEC at VEC (tid + i blockDim).
-template <int VEC, int NV, int RT, int YT, int XT>
-__global__ __launch_bounds__(1024) void k_norm_fwd(NormArgs a)
+// A row's thread has NV groups of eight columns, at 8 (tid + i team).  MAXT = 64: each wave of the block has
+// a row of its own (up to 512 columns); else the block has it.
+template <int MAXT, int NV, bool TAIL, int RT, int YT, int XT>
+__global__ __launch_bounds__(MAXT == 64 ? 64 * kWaveRows : MAXT) void k_norm_fwd(NormArgs a)
 {
+    constexpr bool kWave = MAXT == 64;
     __shared__ float scr[2][16];
-    const int tid = threadIdx.x, D = a.D, t = blockIdx.x;
-    const size_t row = (size_t)t * D;
+    const int team = kWave ? 64 : (int)blockDim.x, tid = kWave ? threadIdx.x & 63 : threadIdx.x, D = a.D;
+    const int first = kWave ? (int)(blockIdx.x * kWaveRows + (threadIdx.x >> 6)) : (int)blockIdx.x;
     const float invD = 1.f / (float)D;
     int turn = 0;
-    float z[NV][VEC];
-#pragma unroll
-    for (int i = 0; i < NV; i++) {
-        const int c = VEC * (tid + i * (int)blockDim.x);
-        if (c < D)
-            ld_vec<VEC>(a.r, RT, row + c, z[i]);
-        else
-#pragma unroll
-            for (int e = 0; e < VEC; e++) z[i][e] = 0.f;
-    }
-    if (a.y) {
-        float y[NV][VEC], ss = 0.f, ry = 1.f;
+    const int t = first;
+    if (t >= a.T) return;
+    const size_t row = (size_t)t * D;
+    const bool full = a.gate == GATE_FULL && a.y;
+    float z[NV][8], y[NV][8], g[NV][8];
+    {
+        Raw<RT, TAIL> nr[NV];
+        Raw<YT, TAIL> ny[NV], ng[NV];
 #pragma unroll
         for (int i = 0; i < NV; i++) {
-            const int c = VEC * (tid + i * (int)blockDim.x);
-            if (c < D)
-                ld_vec<VEC>(a.y, YT, row + c, y[i]);
-            else
-#pragma unroll
-                for (int e = 0; e < VEC; e++) y[i][e] = 0.f;
+            const int c = 8 * (tid + i * team);
+            if (c >= D) continue;
+            nr[i].load(a.r, row + c, D - c);
+            if (a.y) ny[i].load(a.y, row + c, D - c);
+            if (full) ng[i].load(a.g, row + c, D - c);
         }
+        const float tg = a.gate == GATE_TOKEN && a.y ? a.beta * ((const float *)a.g)[t] : a.beta;
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const bool in = 8 * (tid + i * team) < D;
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                z[i][e] = in ? nr[i].at(e) : 0.f;
+                y[i][e] = in && a.y ? ny[i].at(e) : 0.f;
+                g[i][e] = in && full ? tg * ng[i].at(e) : tg;
+            }
+        }
+    }
+    if (a.y) {
+        float ss = 0.f, ry = 1.f;
         if (a.post) {
 #pragma unroll
             for (int i = 0; i < NV; i++)
 #pragma unroll
-                for (int e = 0; e < VEC; e++) ss += y[i][e] * y[i][e];
-            ss = block_sum(ss, scr, turn);
+                for (int e = 0; e < 8; e++) ss += y[i][e] * y[i][e];
+            ss = row_sum<kWave>(ss, scr, turn);
             ry = 1.f / sqrtf(ss * invD + a.eps_post);
             if (a.rstd && tid == 0) a.rstd[t] = ry;
         }
-        float tg = a.beta;
-        if (a.gate == GATE_TOKEN) tg *= ((const float *)a.g)[t];
 #pragma unroll
         for (int i = 0; i < NV; i++) {
-            const int c = VEC * (tid + i * (int)blockDim.x);
+            const int c = 8 * (tid + i * team);
             if (c >= D) continue;
-            float w[VEC], g[VEC];
+            float w[8];
             if (a.post) {
-                ld_vec<VEC>(a.w_post, a.wt, c, w);
+                ld_vec<TAIL>(a.w_post, a.wt, c, D - c, w);
 #pragma unroll
-                for (int e = 0; e < VEC; e++) y[i][e] = y[i][e] * ry * w[e];
+                for (int e = 0; e < 8; e++) y[i][e] = y[i][e] * ry * w[e];
             }
-            if (a.gate == GATE_CHANNEL) ld_vec<VEC>(a.g, DT_F32, c, g);
-            if (a.gate == GATE_FULL) ld_vec<VEC>(a.g, YT, row + c, g);
+            if (a.gate == GATE_CHANNEL) {
+                ld_vec<TAIL>(a.g, DT_F32, c, D - c, w);
 #pragma unroll
-            for (int e = 0; e < VEC; e++) {
-                const float s = a.gate == GATE_CHANNEL || a.gate == GATE_FULL ? tg * g[e] : tg;
-                z[i][e] = a.alpha * z[i][e] + s * y[i][e];
+                for (int e = 0; e < 8; e++) g[i][e] *= w[e];
             }
-            round_to<VEC>(RT, z[i]);
-            st_vec<VEC>(a.r_out, RT, row + c, z[i]);
+#pragma unroll
+            for (int e = 0; e < 8; e++) z[i][e] = a.alpha * z[i][e] + g[i][e] * y[i][e];
+            round_to(RT, z[i]);
+            st_vec<TAIL>(a.r_out, RT, row + c, D - c, z[i]);
         }
     }
     if (!a.next) return;
@@ -157,138 +225,166 @@ __global__ __launch_bounds__(1024) void k_norm_fwd(NormArgs a)
 #pragma unroll
     for (int i = 0; i < NV; i++)
 #pragma unroll
-        for (int e = 0; e < VEC; e++) ss += z[i][e] * z[i][e];
-    ss = block_sum(ss, scr, turn);
+        for (int e = 0; e < 8; e++) ss += z[i][e] * z[i][e];
+    ss = row_sum<kWave>(ss, scr, turn);
     const float rz = 1.f / sqrtf(ss * invD + a.eps_next);
     if (a.rstd && tid == 0) a.rstd[a.T + t] = rz;
 #pragma unroll
     for (int i = 0; i < NV; i++) {
-        const int c = VEC * (tid + i * (int)blockDim.x);
+        const int c = 8 * (tid + i * team);
         if (c >= D) continue;
-        float w[VEC];
-        ld_vec<VEC>(a.w_next, a.wt, c, w);
+        float w[8];
+        ld_vec<TAIL>(a.w_next, a.wt, c, D - c, w);
 #pragma unroll
-        for (int e = 0; e < VEC; e++) w[e] = z[i][e] * rz * w[e];
-        st_vec<VEC>(a.x, XT, row + c, w);
+        for (int e = 0; e < 8; e++) w[e] = z[i][e] * rz * w[e];
+        st_vec<TAIL>(a.x, XT, row + c, D - c, w);
     }
 }
 
-template <int VEC, int NV, int RT, int YT, int XT>
-__global__ __launch_bounds__(1024) void k_norm_bwd(NormArgs a)
+// FULL: the gate is MOE_GATE_FULL (its row held beside the others).
+template <int MAXT, int NV, bool TAIL, bool FULL, int RT, int YT, int XT>
+__global__ __launch_bounds__(MAXT == 64 ? 64 * kWaveRows : MAXT) void k_norm_bwd(NormArgs a)
 {
+    constexpr bool kWave = MAXT == 64;
     __shared__ float scr[2][16];
-    const int tid = threadIdx.x, D = a.D;
+    const int team = kWave ? 64 : (int)blockDim.x, tid = kWave ? threadIdx.x & 63 : threadIdx.x, D = a.D;
+    const int first = kWave ? (int)(blockIdx.x * kWaveRows + (threadIdx.x >> 6)) : (int)blockIdx.x;
     const float invD = 1.f / (float)D;
     int turn = 0;
-    float s1[NV][VEC], s2[NV][VEC], sg[NV][VEC];
+    if (kWave && first >= a.T) return;  // a wave without a row has no partial row either
+    float s1[NV][8], s2[NV][8], sg[NV][8];
 #pragma unroll
     for (int i = 0; i < NV; i++)
 #pragma unroll
-        for (int e = 0; e < VEC; e++) s1[i][e] = s2[i][e] = sg[i][e] = 0.f;
+        for (int e = 0; e < 8; e++) s1[i][e] = s2[i][e] = sg[i][e] = 0.f;
 
-    for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+    Raw<RT, TAIL> nd[NV], nz[NV];
+    Raw<YT, TAIL> ny[NV], ng[FULL ? NV : 1];
+    Raw<XT, TAIL> nx[NV];
+    float nrz = 0.f, nry = 1.f, ngt = 1.f;
+    const bool token = a.gate == GATE_TOKEN && a.y;
+    auto fetch = [&](int t) {
         const size_t row = (size_t)t * D;
-        float d[NV][VEC], y[NV][VEC], dxw[NV][VEC];
-        const float rz = a.next ? a.rstd[a.T + t] : 0.f;
-        const float ry = a.y && a.post ? a.rstd[t] : 1.f;
-        float c2 = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; i++) {
-            const int c = VEC * (tid + i * (int)blockDim.x);
-            const bool in = c < D;
-#pragma unroll
-            for (int e = 0; e < VEC; e++) d[i][e] = y[i][e] = dxw[i][e] = 0.f;
-            if (!in) continue;
-            if (a.dr_out) ld_vec<VEC>(a.dr_out, RT, row + c, d[i]);
-            if (a.y) ld_vec<VEC>(a.y, YT, row + c, y[i]);
+            const int c = 8 * (tid + i * team);
+            if (c >= D) continue;
             if (a.next) {
-                float z[VEC], w[VEC];
-                ld_vec<VEC>(a.dx, XT, row + c, dxw[i]);
-                ld_vec<VEC>(a.r_out, RT, row + c, z);
-                ld_vec<VEC>(a.w_next, a.wt, c, w);
+                nx[i].load(a.dx, row + c, D - c);
+                nz[i].load(a.r_out, row + c, D - c);
+            }
+            if (a.dr_out) nd[i].load(a.dr_out, row + c, D - c);
+            if (a.y) ny[i].load(a.y, row + c, D - c);
+            if constexpr (FULL) ng[i].load(a.g, row + c, D - c);
+        }
+        if (a.next) nrz = a.rstd[a.T + t];
+        if (a.y && a.post) nry = a.rstd[t];
+        if (token) ngt = ((const float *)a.g)[t];
+    };
+    // the next row is requested before the present one is worked on, where the registers hold both
+    constexpr bool kAhead = NV == 1;
+    const int stride = kWave ? (int)gridDim.x * kWaveRows : (int)gridDim.x;
+    if (kAhead && first < a.T) fetch(first);
+    for (int t = first; t < a.T; t += stride) {
+        if (!kAhead) fetch(t);
+        const size_t row = (size_t)t * D;
+        float d[NV][8], y[NV][8], g[FULL ? NV : 1][8], dxw[NV][8], zn[NV][8];
+        const float rz = nrz, ry = nry, gt = ngt;
 #pragma unroll
-                for (int e = 0; e < VEC; e++) {
-                    const float zn = z[e] * rz;
-                    s2[i][e] += dxw[i][e] * zn;
-                    dxw[i][e] *= w[e];
-                    c2 += dxw[i][e] * zn;
-                }
+        for (int i = 0; i < NV; i++) {
+            const bool in = 8 * (tid + i * team) < D;
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                d[i][e] = in && a.dr_out ? nd[i].at(e) : 0.f;
+                y[i][e] = in && a.y ? ny[i].at(e) * ry : 0.f;  // y hat
+                if constexpr (FULL) g[i][e] = in ? ng[i].at(e) : 0.f;
+                dxw[i][e] = in && a.next ? nx[i].at(e) : 0.f;
+                zn[i][e] = in && a.next ? nz[i].at(e) * rz : 0.f;
             }
         }
+        if (kAhead && t + stride < a.T) fetch(t + stride);
         if (a.next) {
-            c2 = block_sum(c2, scr, turn) * invD;
+            float c2 = 0.f;
 #pragma unroll
             for (int i = 0; i < NV; i++) {
-                const int c = VEC * (tid + i * (int)blockDim.x);
+                const int c = 8 * (tid + i * team);
                 if (c >= D) continue;
-                float z[VEC];
-                ld_vec<VEC>(a.r_out, RT, row + c, z);
+                float w[8];
+                ld_vec<TAIL>(a.w_next, a.wt, c, D - c, w);
 #pragma unroll
-                for (int e = 0; e < VEC; e++) d[i][e] += rz * (dxw[i][e] - z[e] * rz * c2);
+                for (int e = 0; e < 8; e++) {
+                    s2[i][e] += dxw[i][e] * zn[i][e];
+                    dxw[i][e] *= w[e];
+                    c2 += dxw[i][e] * zn[i][e];
+                }
             }
+            c2 = row_sum<kWave>(c2, scr, turn) * invD;
+#pragma unroll
+            for (int i = 0; i < NV; i++)
+#pragma unroll
+                for (int e = 0; e < 8; e++) d[i][e] += rz * (dxw[i][e] - zn[i][e] * c2);
         }
         if (!a.y) {
 #pragma unroll
             for (int i = 0; i < NV; i++) {
-                const int c = VEC * (tid + i * (int)blockDim.x);
-                if (c < D) st_vec<VEC>(a.dr, RT, row + c, d[i]);
+                const int c = 8 * (tid + i * team);
+                if (c < D) st_vec<TAIL>(a.dr, RT, row + c, D - c, d[i]);
             }
             continue;
         }
-        const float gt = a.gate == GATE_TOKEN ? ((const float *)a.g)[t] : 1.f;
-        // S = mean over the row of (gate) d w1 yhat, the gate of a token left out
+        // S: sum over the row of beta (gate) d w1 yhat, the gate of a token left out
         float S = 0.f;
-        float dn[NV][VEC];
 #pragma unroll
         for (int i = 0; i < NV; i++) {
-            const int c = VEC * (tid + i * (int)blockDim.x);
-#pragma unroll
-            for (int e = 0; e < VEC; e++) dn[i][e] = 0.f;
+            const int c = 8 * (tid + i * team);
             if (c >= D) continue;
-            float w[VEC], g[VEC], o[VEC];
+            float w[8], o[8];
 #pragma unroll
-            for (int e = 0; e < VEC; e++) w[e] = 1.f, g[e] = 1.f;
-            if (a.post) ld_vec<VEC>(a.w_post, a.wt, c, w);
-            if (a.gate == GATE_CHANNEL) ld_vec<VEC>(a.g, DT_F32, c, g);
-            if (a.gate == GATE_FULL) ld_vec<VEC>(a.g, YT, row + c, g);
+            for (int e = 0; e < 8; e++) o[e] = a.alpha * d[i][e];
+            st_vec<TAIL>(a.dr, RT, row + c, D - c, o);
+            float gc[8];
 #pragma unroll
-            for (int e = 0; e < VEC; e++) o[e] = a.alpha * d[i][e];
-            st_vec<VEC>(a.dr, RT, row + c, o);
+            for (int e = 0; e < 8; e++) w[e] = 1.f, gc[e] = 1.f;
+            if constexpr (FULL) {
 #pragma unroll
-            for (int e = 0; e < VEC; e++) {
-                const float yh = y[i][e] * ry, bd = a.beta * d[i][e];
-                o[e] = bd * yh * w[e];                       // beta d n
-                const float q = bd * g[e];                   // dn without a token's gate
-                s1[i][e] += q * gt * yh;
-                sg[i][e] += o[e];
-                dn[i][e] = q * w[e];
-                S += dn[i][e] * yh;
-                y[i][e] = yh;
+                for (int e = 0; e < 8; e++) gc[e] = g[i][e];
+            } else {
+                if (a.gate == GATE_CHANNEL) ld_vec<TAIL>(a.g, DT_F32, c, D - c, gc);
             }
-            if (a.gate == GATE_FULL && a.dg) st_vec<VEC>(a.dg, YT, row + c, o);
+            if (a.post) ld_vec<TAIL>(a.w_post, a.wt, c, D - c, w);
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                const float bd = a.beta * d[i][e], q = bd * gc[e];  // q: dn without a token's gate
+                o[e] = bd * y[i][e] * w[e];                           // beta d n
+                s1[i][e] += q * gt * y[i][e];
+                sg[i][e] += o[e];
+                d[i][e] = q * w[e];
+                S += d[i][e] * y[i][e];
+            }
+            if (a.gate == GATE_FULL && a.dg) st_vec<TAIL>(a.dg, YT, row + c, D - c, o);
         }
-        if (a.post || (a.gate == GATE_TOKEN && a.dg)) S = block_sum(S, scr, turn);
+        if (a.post || (a.gate == GATE_TOKEN && a.dg)) S = row_sum<kWave>(S, scr, turn);
         if (a.gate == GATE_TOKEN && a.dg && tid == 0) ((float *)a.dg)[t] = S;
         const float cs = a.post ? S * invD : 0.f;
         const float f = gt * ry;
 #pragma unroll
         for (int i = 0; i < NV; i++) {
-            const int c = VEC * (tid + i * (int)blockDim.x);
+            const int c = 8 * (tid + i * team);
             if (c >= D) continue;
-            float o[VEC];
+            float o[8];
 #pragma unroll
-            for (int e = 0; e < VEC; e++) o[e] = f * (dn[i][e] - y[i][e] * cs);
-            st_vec<VEC>(a.dy, YT, row + c, o);
+            for (int e = 0; e < 8; e++) o[e] = f * (d[i][e] - y[i][e] * cs);
+            st_vec<TAIL>(a.dy, YT, row + c, D - c, o);
         }
     }
-    float *p = a.part + (size_t)blockIdx.x * 3 * D;
+    float *p = a.part + (size_t)first * 3 * D;
 #pragma unroll
     for (int i = 0; i < NV; i++) {
-        const int c = VEC * (tid + i * (int)blockDim.x);
+        const int c = 8 * (tid + i * team);
         if (c >= D) continue;
-        if (a.dw_post) st_vec<VEC>(p, DT_F32, c, s1[i]);
-        if (a.dw_next) st_vec<VEC>(p + D, DT_F32, c, s2[i]);
-        if (a.gate == GATE_CHANNEL && a.dg) st_vec<VEC>(p + 2 * (size_t)D, DT_F32, c, sg[i]);
+        if (a.dw_post) st_vec<TAIL>(p, DT_F32, c, D - c, s1[i]);
+        if (a.dw_next) st_vec<TAIL>(p + D, DT_F32, c, D - c, s2[i]);
+        if (a.gate == GATE_CHANNEL && a.dg) st_vec<TAIL>(p + 2 * (size_t)D, DT_F32, c, D - c, sg[i]);
     }
 }
 
@@ -303,18 +399,21 @@ __global__ __launch_bounds__(1024) void k_norm_cols(NormArgs a, int nb)
     const int per = (nb + 31) / 32;
     float v = 0.f;
     if (c < a.D)
+#pragma unroll 8
         for (int b = rg * per; b < min(nb, (rg + 1) * per); b++) v += a.part[((size_t)b * 3 + q) * a.D + c];
     s[rg][cx] = v;
     __syncthreads();
     if (rg == 0 && c < a.D) {
         v = 0.f;
         for (int k = 0; k < 32; k++) v += s[k][cx];
-        const float o[1] = {v};
-        st_vec<1>(out, q == 2 ? DT_F32 : a.wt, c, o);
+        if (q == 2 || a.wt == DT_F32)
+            ((float *)out)[c] = v;
+        else
+            ((uint16_t *)out)[c] = (uint16_t)pack_bf16(v, 0.f);
     }
 }
 
-bool wide(const NormArgs &a)
+bool aligned16(const NormArgs &a)
 {
     if (a.D % 8) return false;
     for (const void *p : {a.w_post, a.w_next, a.r, a.y, a.g, (const void *)a.r_out, (const void *)a.x, a.dr_out, a.dx, (const void *)a.dr,
@@ -323,32 +422,38 @@ bool wide(const NormArgs &a)
     return true;
 }
 
-// Threads so that NV groups of VEC cover the row with few idle lanes.
-int threads_for(int D, int vec, int nv)
-{
-    const int groups = (D + vec - 1) / vec;
-    return 64 * ((groups + 64 * nv - 1) / (64 * nv));
-}
-
-template <int VEC, int NV, int RT, int YT, int XT>
+template <int MAXT, int NV, bool TAIL, int RT, int YT, int XT>
 void go(const NormArgs &a, bool bwd, int grid, hipStream_t s)
 {
-    const int th = threads_for(a.D, VEC, NV);
-    if (bwd)
-        hipLaunchKernelGGL((k_norm_bwd<VEC, NV, RT, YT, XT>), dim3(grid), dim3(th), 0, s, a);
+    const int groups = (a.D + 7) / 8, th = MAXT == 64 ? 64 * kWaveRows : 64 * ((groups + 64 * NV - 1) / (64 * NV));  // few idle lanes
+    if (MAXT == 64) grid = (grid + kWaveRows - 1) / kWaveRows;
+    if (bwd && a.gate == GATE_FULL && a.y)
+        hipLaunchKernelGGL((k_norm_bwd<MAXT, NV, TAIL, true, RT, YT, XT>), dim3(grid), dim3(th), 0, s, a);
+    else if (bwd)
+        hipLaunchKernelGGL((k_norm_bwd<MAXT, NV, TAIL, false, RT, YT, XT>), dim3(grid), dim3(th), 0, s, a);
     else
-        hipLaunchKernelGGL((k_norm_fwd<VEC, NV, RT, YT, XT>), dim3(grid), dim3(th), 0, s, a);
+        hipLaunchKernelGGL((k_norm_fwd<MAXT, NV, TAIL, RT, YT, XT>), dim3(grid), dim3(th), 0, s, a);
+}
+
+template <bool TAIL, int RT, int YT, int XT>
+void go_width(const NormArgs &a, bool bwd, int grid, hipStream_t s)
+{
+    // a wave a row up to 512 columns (16384 rows of 128: 64 -> 37 us)
+    if (a.D <= kWaveWidth)
+        go<64, 1, TAIL, RT, YT, XT>(a, bwd, grid, s);
+    else if (a.D <= 8192)
+        go<1024, 1, TAIL, RT, YT, XT>(a, bwd, grid, s);
+    else
+        go<1024, 2, TAIL, RT, YT, XT>(a, bwd, grid, s);
 }
 
 template <int RT, int YT, int XT>
 void go_types(const NormArgs &a, bool bwd, int grid, hipStream_t s)
 {
-    if (!wide(a))
-        go<1, 16, RT, YT, XT>(a, bwd, grid, s);
-    else if (a.D <= 8192)
-        go<8, 1, RT, YT, XT>(a, bwd, grid, s);
+    if (aligned16(a))
+        go_width<false, RT, YT, XT>(a, bwd, grid, s);
     else
-        go<8, 2, RT, YT, XT>(a, bwd, grid, s);
+        go_width<true, RT, YT, XT>(a, bwd, grid, s);
 }
 
 void dispatch(const NormArgs &a, bool bwd, int grid, hipStream_t s)
@@ -375,7 +480,7 @@ hipError_t launch_norm_forward(const NormArgs &a, hipStream_t s)
 
 hipError_t launch_norm_backward(const NormArgs &a, hipStream_t s)
 {
-    const int nb = a.T < kNormBlocks ? a.T : kNormBlocks;  // 0 rows: the column sums are zero
+    const int most = norm_parts(a.D), nb = a.T < most ? a.T : most;  // 0 rows: the column sums are zero
     if (nb > 0) dispatch(a, true, nb, s);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !(a.dw_post || a.dw_next || (a.gate == GATE_CHANNEL && a.dg))) return e;

@@ -85,8 +85,8 @@ def test_widths(T, D):
     check(T, D)
 
 
-@pytest.mark.parametrize("T", [2, 511, 512, 513, 1700])
-@pytest.mark.parametrize("D", [40, 33])
+@pytest.mark.parametrize("T", [2, 7, 8, 9, 511, 512, 513, 4097, 9000])
+@pytest.mark.parametrize("D", [40, 33, 520, 515])
 def test_row_counts_with_every_gradient(T, D):
     check(T, D, gate="channel")
 
