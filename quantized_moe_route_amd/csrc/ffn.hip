@@ -652,30 +652,31 @@ hipError_t go(GemmArgs g, int splits, int slots, hipStream_t s)
 // Microseconds that a product is expected to take with BM x BN tiles and its reduction cut in `splits`.
 // From timings of the five products at 1 to 8192 tokens, widths 512 to 14336 (the choice is within 10 % of
 // the best tile and split of each): a step of 32 k on one CU takes 0.72 us for a 256 x 256 tile, 0.27 for
-// 128 x 128 (two blocks share a CU, 0.55 for both) and 0.145 for 64 x 64 (four blocks; 0.21 alone), so a
+// 128 x 128 (two blocks share a CU, 0.55 for both; 0.24 alone, 0.36 waiting for memory) and 0.145 for 64 x 64
+// (four blocks; 0.21, 0.31 alone), so a
 // large tile does 1.5 and 3 times the work of the smaller ones in the same time, and wins where it fills
 // the card: 4096 tokens down 147 us against 223 and 381, but 1024 tokens d h 93 against 67 and 91.  What
 // comes back from a cut reduction crosses memory twice more in fp32 (6144 -> 3584 at 64 tokens: whole 41 us,
-// in eight parts 19).  Memory brings what the resident blocks have asked for, three steps each, in about a
-// microsecond.
+// in eight parts 20).  Memory brings what the resident blocks have asked for, three steps each, in 1.2 us.
 struct Shape {
     int tile, resident;
-    double step, alone, tail;  // us per step beside others, per step alone, per tile's end
+    double step, cached, alone, tail;  // us per step beside others, per step alone (operands in the last-level cache, in memory), per tile's end
 };
-constexpr Shape kShapes[3] = {{256, 1, 0.72, 0.54, 6.0}, {128, 2, 0.27, 0.24, 1.5}, {64, 4, 0.145, 0.21, 0.5}};
+constexpr Shape kShapes[3] = {{256, 1, 0.72, 0.54, 0.60, 6.0}, {128, 2, 0.27, 0.24, 0.355, 1.5}, {64, 4, 0.145, 0.21, 0.31, 0.5}};
+constexpr double kCached = 32e6;  // operands of fewer bytes are taken to be still cached from the call before
 
 double expected_us(const Shape &c, int64_t tiles, int64_t steps, int splits, int cus, int rows, double in_bytes, double out_bytes,
                    double part_bytes)
 {
     const int64_t per = ((steps + splits - 1) / splits + kBufs - 1) / kBufs * kBufs, parts = (steps + per - 1) / per;
     const int64_t blocks = tiles * parts, n = (blocks + cus - 1) / cus;  // n: tiles of the busiest CU
-    const double one = c.step * n > c.alone ? c.step * n : c.alone;
+    const double alone = in_bytes < kCached ? c.cached : c.alone, one = c.step * n > alone ? c.step * n : alone;
     double work = per * one + c.tail * n;
     const int64_t resident = blocks < (int64_t)c.resident * cus ? blocks : (int64_t)c.resident * cus;
     const double asked = (double)resident * (kBufs - 1) * kBK * 2 * (c.tile + (rows < c.tile ? rows : c.tile));
-    const double mem = in_bytes / (asked < 4.5e6 ? asked : 4.5e6);
+    const double rate = asked / 1.2 < 5e6 ? asked / 1.2 : 5e6, mem = in_bytes / rate;
     if (mem > work) work = mem;
-    return 4.0 + work + out_bytes / 4.4e6 + (parts > 1 ? 4.0 + 2.0 * parts * part_bytes / 5e6 : 0.0);
+    return 3.0 + work + out_bytes / 4.4e6 + (parts > 1 ? 2.0 + 2.0 * parts * part_bytes / 5e6 : 0.0);
 }
 
 struct Plan {
