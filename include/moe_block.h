@@ -149,7 +149,7 @@ void moe_norm_destroy(moe_norm *h);
  *
  * MOE_STATE_E4M3 keeps m and sqrt(v) as OCP E4M3 codes, one byte each, with an fp32 scale for each
  * run of 256 consecutive elements of a tensor (the last run may be shorter): scale = max|.| / 448,
- * code = rne(value * (1 / scale)), value = code * scale.  A run whose scale is below 2^-126 is stored as
+ * code = rne(value / scale), value = code * scale.  A run whose scale is below 2^-126 is stored as
  * zeros; a positive sqrt(v) is never stored as code zero (it takes the smallest code), so a decayed
  * moment is not divided by a lost one.  The parameter update uses the unquantized new moments. */
 typedef enum { MOE_STATE_F32 = 0, MOE_STATE_E4M3 = 1 } moe_state_fmt;

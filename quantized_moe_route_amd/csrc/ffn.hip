@@ -87,16 +87,18 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b)
 
 // One operand's tile of ROWS rows (of the output side) by kBK: its loader and its MFMA fragments.
 // KM = false: stored [row][k], LDS [row][32] with the 16-byte chunk c of row r at c ^ (r / 4 % 4).
-// KM = true: stored [k][row], LDS [k][ROWS] with chunk c of k at c ^ (4 (k % 4)) (64 rows: 4 (k % 2)):
-//   the four k of a transposing read's 16 lanes fall into four 64-byte groups.
+// KM = true: stored [k][row], LDS [k][ROWS] with chunk c of k at c ^ (4 (k % 4)) (see swz): the four k of a
+//   transposing read's 16 lanes fall into four 64-byte groups.
 // Either way no LDS access of a wave meets a bank twice.  SPAN: the rows of one matrix that the tile
 // covers (half of it where it holds two).
 template <int ROWS, bool KM, int NW, int SPAN = ROWS>
 struct Tile {
-    static constexpr int kSwz = (ROWS / 8 - 1) & 12;
+    // 256 bytes hold 64 banks: rows of a multiple of them are told apart by two bits of k, 192 rows (384
+    // bytes: every second k begins in the other half) and 64 rows by one
+    static constexpr int swz(int k) { return ROWS % 128 == 0 ? (k & 3) << 2 : ROWS > 128 ? (k & 2) << 1 : (k & 1) << 2; }
     static constexpr int kInstr = ROWS * kBK * 2 / 1024 / NW;  // 1 KB loads per wave
     static_assert(kInstr >= 1 && kInstr * NW * 1024 == ROWS * kBK * 2, "tile split over the waves");
-    static_assert(!KM || (ROWS / 8 & (ROWS / 8 - 1)) == 0 || ROWS % 128 == 64, "swizzle stays in the row");
+    static_assert(ROWS % 64 == 0, "a chunk's swizzle stays in its row");
     int chunk[kInstr];      // first k (KM: row) of this lane's piece i
     int line[kInstr];       // its row (KM: k)
     uint32_t voff[kInstr];  // its byte offset in the present product's operand
@@ -113,7 +115,7 @@ struct Tile {
                 constexpr int cpr = ROWS / 8;  // chunks per k
                 const int s = 64 * (wv * kInstr + i) + lane;
                 line[i] = s / cpr;
-                chunk[i] = 8 * ((s % cpr) ^ ((line[i] << 2) & kSwz));
+                chunk[i] = 8 * ((s % cpr) ^ swz(line[i]));
             }
         }
     }
@@ -163,7 +165,7 @@ struct Tile {
             // 16-lane group q: rows 16 (q % 2), k from 8 (q / 2); lane i of it addresses k i / 4, rows 4 (i % 4)
             const int q = lane >> 4, i = lane & 15;
             const int k = 16 * s + 8 * (q >> 1) + (i >> 2), row = row0 + 16 * (q & 1) + 4 * (i & 3);
-            const uint16_t *p = lds + k * ROWS + ((row & ~7) ^ (((k << 2) & kSwz) << 3)) + (row & 7);
+            const uint16_t *p = lds + k * ROWS + ((row & ~7) ^ (swz(k) << 3)) + (row & 7);
             const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16 *)p);
             const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16 *)(p + 4 * ROWS));
             const u32x2 l2 = __builtin_bit_cast(u32x2, lo), h2 = __builtin_bit_cast(u32x2, hi);
@@ -659,10 +661,13 @@ hipError_t go(GemmArgs g, int splits, int slots, hipStream_t s)
 // comes back from a cut reduction crosses memory twice more in fp32 (6144 -> 3584 at 64 tokens: whole 41 us,
 // in eight parts 20).  Memory brings what the resident blocks have asked for, three steps each, in 1.2 us.
 struct Shape {
-    int tile, resident;
+    int rows, cols, resident;
     double step, cached, alone, tail;  // us per step beside others, per step alone (operands in the last-level cache, in memory), per tile's end
 };
-constexpr Shape kShapes[3] = {{256, 1, 0.72, 0.54, 0.60, 6.0}, {128, 2, 0.27, 0.24, 0.355, 1.5}, {64, 4, 0.145, 0.21, 0.31, 0.5}};
+constexpr Shape kShapes[4] = {{256, 256, 1, 0.72, 0.54, 0.60, 6.0},
+                              {256, 192, 1, 0.64, 0.48, 0.53, 4.5},
+                              {128, 128, 2, 0.27, 0.24, 0.355, 1.5},
+                              {64, 64, 4, 0.145, 0.21, 0.31, 0.5}};
 constexpr double kCached = 32e6;  // operands of fewer bytes are taken to be still cached from the call before
 
 double expected_us(const Shape &c, int64_t tiles, int64_t steps, int splits, int cus, int rows, double in_bytes, double out_bytes,
@@ -673,7 +678,7 @@ double expected_us(const Shape &c, int64_t tiles, int64_t steps, int splits, int
     const double alone = in_bytes < kCached ? c.cached : c.alone, one = c.step * n > alone ? c.step * n : alone;
     double work = per * one + c.tail * n;
     const int64_t resident = blocks < (int64_t)c.resident * cus ? blocks : (int64_t)c.resident * cus;
-    const double asked = (double)resident * (kBufs - 1) * kBK * 2 * (c.tile + (rows < c.tile ? rows : c.tile));
+    const double asked = (double)resident * (kBufs - 1) * kBK * 2 * (c.cols + (rows < c.rows ? rows : c.rows));
     const double rate = asked / 1.2 < 5e6 ? asked / 1.2 : 5e6, mem = in_bytes / rate;
     if (mem > work) work = mem;
     return 3.0 + work + out_bytes / 4.4e6 + (parts > 1 ? 2.0 + 2.0 * parts * part_bytes / 5e6 : 0.0);
@@ -701,10 +706,10 @@ Plan plan(GemmArgs &g, size_t part_floats)
                                 : EPI == EPI_GU ? mn * (2 * (g.h ? g.planes : 0) + (g.gu ? 8 : 0)) : mn * (8 + 2 * g.planes * ((g.h ? 1 : 0) + (g.dgu ? 2 : 0)));
         rows = rows > p.M ? rows : p.M;
     }
-    const int64_t tiles[3] = {count_tiles<256, 256, EPI>(g), count_tiles<128, 128, EPI>(g), count_tiles<64, 64, EPI>(g)};
+    const int64_t tiles[4] = {count_tiles<256, 256, EPI>(g), count_tiles<256, 192, EPI>(g), count_tiles<128, 128, EPI>(g), count_tiles<64, 64, EPI>(g)};
     Plan best;
-    for (int c = 0; c < 3; c++)
-        for (int sp = 1; sp <= 16 && (sp == 1 || (steps / sp >= kBufs && floats * sp <= part_floats)); sp++) {
+    for (int c = 0; c < 4; c++)
+        for (int sp = 1; sp <= 16 && !(EPI == EPI_GU && c == 1) && (sp == 1 || (steps / sp >= kBufs && floats * sp <= part_floats)); sp++) {
             const double t = expected_us(kShapes[c], tiles[c], steps, sp, cus, rows, in, out, 4.0 * floats);
             if (t < best.us) best = {c, sp, t};
         }
@@ -721,7 +726,9 @@ hipError_t gemm(GemmArgs g, float *part, size_t part_floats, hipStream_t s)
         part += (size_t)c.splits * g.p[i].M * g.p[i].N * (EPI == EPI_GU ? 2 : 1);
     }
     if (c.shape == 0) return go<256, 256, 2, 2, AK, BKM, EPI, ACT>(g, c.splits, cus, s);
-    if (c.shape == 1) return go<128, 128, 2, 2, AK, BKM, EPI, ACT>(g, c.splits, 2 * cus, s);
+    if constexpr (EPI != EPI_GU)  // gate and up columns pair within a wave: an even number of tiles
+        if (c.shape == 1) return go<256, 192, 2, 2, AK, BKM, EPI, ACT>(g, c.splits, cus, s);
+    if (c.shape == 2) return go<128, 128, 2, 2, AK, BKM, EPI, ACT>(g, c.splits, 2 * cus, s);
     return go<64, 64, 2, 1, AK, BKM, EPI, ACT>(g, c.splits, 4 * cus, s);
 }
 

@@ -31,7 +31,7 @@ def encode(a):
     b = b.view(-1, 256)
     s = b.abs().amax(1) * (1.0 / 448.0)
     s = torch.where(s < 2.0 ** -126, torch.zeros_like(s), s)
-    c = torch.where(s[:, None] == 0, torch.zeros_like(b), b * (1.0 / torch.where(s == 0, torch.ones_like(s), s))[:, None]).to(E4M3)
+    c = torch.where(s[:, None] == 0, torch.zeros_like(b), b / torch.where(s == 0, torch.ones_like(s), s)[:, None]).to(E4M3)
     return c.view(torch.uint8).view(-1)[:n].view(a.shape), s
 
 

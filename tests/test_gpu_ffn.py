@@ -59,18 +59,20 @@ def test_forward_and_gradients(T, D, I, act, dt):
             close(a, b, dt, K, n)
 
 
-def test_large_tiles():
-    T, D, I = 3300, 4104, 2056
+# sizes at which the five products take, among them, every tile shape, whole and with the reduction in parts
+@pytest.mark.parametrize("T,D,I", [(3300, 4104, 2056), (4096, 1024, 6144), (4000, 512, 3080), (1030, 520, 4104), (48, 2048, 3000)])
+def test_every_tile_shape(T, D, I):
     c = make(T, D, I)
     f = layer(c, T)
     for dt in (BF16, F32):
         gu = f.new_saved_gu(T)
         y = f.forward(c["x"], out_dtype=dt, saved_gu=gu)
         want, _ = ref.ffn_grads("swiglu", *(c[k] for k in ("x", "wg", "wu", "wd", "dy")))
-        close(y, ref.ffn("swiglu", c["x"], c["wg"], c["wu"], c["wd"]), dt, D, "y")
+        K = max(T, D, 2 * I)
+        close(y, ref.ffn("swiglu", c["x"], c["wg"], c["wu"], c["wd"]), dt, K, "y")
         got = f.backward(c["x"], c["dy"], saved_gu=gu, dx_dtype=dt, dw_dtype=dt)
         for a, b, n in zip((got[0], *got[1]), want, ("dx", "dw_gate", "dw_up", "dw_down")):
-            close(a, b, dt, D, n)
+            close(a, b, dt, K, n)
 
 
 @pytest.mark.parametrize("T,D,I", [(1, 256, 128), (5, 264, 136), (100, 328, 264)])
