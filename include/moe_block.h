@@ -37,9 +37,9 @@ extern "C" {
  * result h = act(g, u) is rounded once to bf16 (2^-9 relative at most), for an fp32 result h
  * enters as three bf16 terms that hold its 24 bits.  The gradients' dg and du likewise. */
 typedef struct {
-    int32_t width;       /* D: multiple of 8 */
-    int32_t inter;       /* I: multiple of 8 */
-    int32_t max_tokens;  /* largest T of any call; sizes the workspace */
+    int32_t width;       /* D: multiple of 8, at most 2^20 */
+    int32_t inter;       /* I: multiple of 8, at most 2^20 */
+    int32_t max_tokens;  /* largest T of any call, at most 2^24; sizes the workspace */
     int32_t act;         /* moe_act */
     uint32_t flags;      /* MOE_FFN_* */
 } moe_ffn_desc;
@@ -99,7 +99,7 @@ enum {
 
 typedef struct {
     int32_t width;       /* D: 1..16384 */
-    int32_t max_tokens;
+    int32_t max_tokens;  /* 0..2^30 */
     int32_t r_dtype, y_dtype, x_dtype, w_dtype;  /* moe_dtype: residual, block output, next input, norm weights */
     int32_t gate;        /* moe_gate */
     float eps_post, eps_next;  /* > 0 */

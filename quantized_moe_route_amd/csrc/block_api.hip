@@ -119,7 +119,7 @@ moe_status check_norm_desc(const moe_norm_desc *d)
     if (!d) return api_fail(MOE_ERR_INVALID_ARG, "desc is NULL");
     if (d->width <= 0 || d->width > moe::kMaxNormWidth)
         return api_fail(MOE_ERR_INVALID_ARG, "width=%d must be in 1..%d", d->width, moe::kMaxNormWidth);
-    if (d->max_tokens < 0) return api_fail(MOE_ERR_INVALID_ARG, "max_tokens=%d is negative", d->max_tokens);
+    if (d->max_tokens < 0 || d->max_tokens > (1 << 30)) return api_fail(MOE_ERR_INVALID_ARG, "max_tokens=%d must be in 0..2^30", d->max_tokens);
     if (!is_dtype(d->r_dtype) || !is_dtype(d->y_dtype) || !is_dtype(d->x_dtype) || !is_dtype(d->w_dtype))
         return api_fail(MOE_ERR_INVALID_ARG, "a dtype (r %d, y %d, x %d, w %d) is not f32/bf16", d->r_dtype, d->y_dtype,
                         d->x_dtype, d->w_dtype);

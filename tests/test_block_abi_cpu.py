@@ -28,7 +28,7 @@ def size(kind, d):
 @pytest.mark.parametrize("kind,bad", [
     ("ffn", [dict(width=0), dict(width=12), dict(width=-8), dict(inter=0), dict(inter=20), dict(width=(1 << 20) + 8), dict(max_tokens=-1),
              dict(act=2), dict(act=-1), dict(flags=2)]),
-    ("norm", [dict(width=0), dict(width=16385), dict(max_tokens=-1), dict(r_dtype=2), dict(y_dtype=-1), dict(x_dtype=9), dict(w_dtype=5),
+    ("norm", [dict(width=0), dict(width=16385), dict(max_tokens=-1), dict(max_tokens=(1 << 30) + 1), dict(r_dtype=2), dict(y_dtype=-1), dict(x_dtype=9), dict(w_dtype=5),
               dict(gate=4), dict(gate=-1), dict(eps_post=0.0), dict(eps_next=-1.0), dict(eps_post=float("nan")),
               dict(res_scale=float("inf")), dict(branch_scale=float("nan")), dict(flags=8)]),
     ("adamw", [dict(beta1=1.0), dict(beta2=-0.1), dict(beta1=float("nan")), dict(eps=0.0), dict(eps=1e-60), dict(max_norm=-1.0),

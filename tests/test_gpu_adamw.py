@@ -139,6 +139,32 @@ def test_unaligned_views_and_many_tensors():
             assert ((got.to(F64) - x).abs() <= 16 * U * (x.abs() + 0.2) + 1e-12).all(), i
 
 
+@pytest.mark.parametrize("pt", [F32, BF16])
+@pytest.mark.parametrize("clip", [0.0, 0.3])
+def test_8bit_states_at_any_alignment_have_the_same_bits(pt, clip):
+    """Views that begin anywhere take the element-wise loads: the same arithmetic."""
+    sizes = [1 + (i * 211) % 1900 for i in range(60)]
+    n = sum(sizes)
+    w, g = (torch.randn(n, device="cuda") * s for s in (0.02, 2e-3))
+
+    def run(shift):
+        bank = lambda t, dt: torch.cat([torch.zeros(shift, device="cuda"), t]).to(dt)[shift:].split(sizes)  # noqa: E731
+        p, gr = bank(w, pt), bank(g, pt)
+        if not shift:  # buffers of their own
+            p, gr = [t.clone() for t in p], [t.clone() for t in gr]
+        codes = [list(torch.zeros(n + shift, device="cuda", dtype=torch.uint8)[shift:].split(sizes)) for _ in range(2)]
+        st = q.AdamW.new_state(p, e4m3=True) | (dict(m=codes[0], v=codes[1]) if shift else {})
+        o = q.AdamW(p, gr, **st, max_norm=clip)
+        for _ in range(3):
+            o.step(1e-2)
+        return p, o
+
+    pa, a = run(0)
+    pb, b = run(1)
+    for x, y in ((pa, pb), (a.m, b.m), (a.v, b.v), (a.m_scale, b.m_scale), (a.v_scale, b.v_scale)):
+        assert all(torch.equal(s, t) for s, t in zip(x, y))
+
+
 @pytest.mark.parametrize("e4m3", [False, True])
 def test_a_norm_that_is_not_finite_skips_the_step(e4m3):
     w, p, g = tensors([(300,), (5, 100)], F32, F32)
