@@ -7,12 +7,12 @@
 //   d x       A = dg | du [T][2I],   B = Wg, Wu [I][D] by k epilogue: dx
 //   d W       A = dg, du or dy by k, B = x or h by k        epilogue: dW
 // "by k": stored [k][n], the reduction over rows.  One kernel template covers them: an operand
-// stored along k is staged in LDS as [row][32 k]; one stored by k as [32 k][row], read with the
+// stored along k is staged in LDS as [row][BK k]; one stored by k as [BK k][row], read with the
 // transposing LDS read.  A product may run over several (A, B) pairs in turn ("segments"): dg and
 // du, and the three bf16 terms of an operand carried exactly.
 //
 // A block owns a BM x BN tile of C at a time; its waves own parts of it as 32 x 32 MFMA tiles.  Both
-// operands stream straight into LDS (16 bytes a lane) into a ring of four buffers of 32 k, three
+// operands stream straight into LDS (16 bytes a lane) into a ring of four buffers of BK k, three
 // steps ahead of the multiplication.  The blocks are persistent: each walks tiles b, b + gridDim, ..., and the stream of
 // loads runs on into the next tile while the present one's results are stored through LDS scratch of
 // their own, so the matrix pipes wait neither for a first load nor for the last store.
@@ -30,7 +30,6 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short v4i16 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
 
-constexpr int kBK = 32;       // reduction indices per step
 constexpr int kBufs = 4;      // LDS buffers of a step each
 constexpr int kMaxSeg = 6;
 constexpr uint32_t kOob = 0x80000000u;  // an offset past every buffer: reads zero
@@ -85,19 +84,22 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b)
     return __builtin_bit_cast(uint32_t, v);
 }
 
-// One operand's tile of ROWS rows (of the output side) by kBK: its loader and its MFMA fragments.
-// KM = false: stored [row][k], LDS [row][32] with the 16-byte chunk c of row r at c ^ (r / 4 % 4).
+// One operand's tile of ROWS rows (of the output side) by BK: its loader and its MFMA fragments.
+// KM = false: stored [row][k], LDS [row][BK] with the 16-byte chunk c of row r at c ^ (r / 4 % 4) (BK = 64:
+//   c ^ (r / 2 % 8)).
 // KM = true: stored [k][row], LDS [k][ROWS] with chunk c of k at c ^ (4 (k % 4)) (see swz): the four k of a
 //   transposing read's 16 lanes fall into four 64-byte groups.
 // Either way no LDS access of a wave meets a bank twice.  SPAN: the rows of one matrix that the tile
 // covers (half of it where it holds two).
-template <int ROWS, bool KM, int NW, int SPAN = ROWS>
+template <int ROWS, int BK, bool KM, int NW, int SPAN = ROWS>
 struct Tile {
     // 256 bytes hold 64 banks: rows of a multiple of them are told apart by two bits of k, 192 rows (384
     // bytes: every second k begins in the other half) and 64 rows by one
     static constexpr int swz(int k) { return ROWS % 128 == 0 ? (k & 3) << 2 : ROWS > 128 ? (k & 2) << 1 : (k & 1) << 2; }
-    static constexpr int kInstr = ROWS * kBK * 2 / 1024 / NW;  // 1 KB loads per wave
-    static_assert(kInstr >= 1 && kInstr * NW * 1024 == ROWS * kBK * 2, "tile split over the waves");
+    static constexpr int kInstr = ROWS * BK * 2 / 1024 / NW;  // 1 KB loads per wave
+    static constexpr int kCpr = BK / 8, kRpi = 64 / kCpr;     // !KM: chunks of a row, rows of a load
+    static constexpr int swz_row(int r) { return BK == 64 ? (r >> 1) & 7 : (r >> 2) & 3; }
+    static_assert(kInstr >= 1 && kInstr * NW * 1024 == ROWS * BK * 2, "tile split over the waves");
     static_assert(ROWS % 64 == 0, "a chunk's swizzle stays in its row");
     int chunk[kInstr];      // first k (KM: row) of this lane's piece i
     int line[kInstr];       // its row (KM: k)
@@ -108,8 +110,8 @@ struct Tile {
 #pragma unroll
         for (int i = 0; i < kInstr; i++) {
             if constexpr (!KM) {
-                line[i] = 16 * (wv * kInstr + i) + (lane >> 2);
-                chunk[i] = 8 * ((lane & 3) ^ ((line[i] >> 2) & 3));
+                line[i] = kRpi * (wv * kInstr + i) + lane / kCpr;
+                chunk[i] = 8 * ((lane % kCpr) ^ swz_row(line[i]));
                 if (SPAN < ROWS) line[i] = 32 * (line[i] >> 6) + (line[i] & 31);  // groups of 32 rows, alternately of two matrices
             } else {
                 constexpr int cpr = ROWS / 8;  // chunks per k
@@ -140,7 +142,7 @@ struct Tile {
             bytes = (uint32_t)(min(left, SPAN) - 1) * ld * 2 + (uint32_t)(K - k0) * 2;
             base += k0;
         } else {
-            bytes = (uint32_t)(min(kBK, K - k0) - 1) * ld * 2 + (uint32_t)left * 2;
+            bytes = (uint32_t)(min(BK, K - k0) - 1) * ld * 2 + (uint32_t)left * 2;
             base += (size_t)k0 * ld;
         }
         return rsrc_of(base, live ? bytes : 0u);
@@ -160,7 +162,7 @@ struct Tile {
     {
         if constexpr (!KM) {
             const int r = row0 + (lane & 31), c = 2 * s + (lane >> 5);
-            return as_bf16x8(*(const u32x4 *)(lds + r * kBK + 8 * (c ^ ((r >> 2) & 3))));
+            return as_bf16x8(*(const u32x4 *)(lds + r * BK + 8 * (c ^ swz_row(r))));
         } else {
             // 16-lane group q: rows 16 (q % 2), k from 8 (q / 2); lane i of it addresses k i / 4, rows 4 (i % 4)
             const int q = lane >> 4, i = lane & 15;
@@ -336,7 +338,8 @@ __device__ __forceinline__ Place place_of(const GemmArgs &g, int v)
 
 // WM x WN waves.  EPI_GU: the B tile holds groups of 32 rows, alternately of the gate and the up
 // matrix, so a wave's column tiles 2 j and 2 j + 1 are gate and up of the same columns.
-template <int BM, int BN, int WM, int WN, bool AK, bool BKM, int EPI, int ACT>
+// BK: reduction indices of a step.
+template <int BM, int BN, int WM, int WN, int BK, bool AK, bool BKM, int EPI, int ACT>
 __global__ __launch_bounds__(64 * WM *WN, 1) void k_ffn_gemm(GemmArgs g)
 {
     constexpr int NW = WM * WN, TM = BM / WM / 32, TN = BN / WN / 32;
@@ -344,21 +347,21 @@ __global__ __launch_bounds__(64 * WM *WN, 1) void k_ffn_gemm(GemmArgs g)
     constexpr int BNC = GU ? BN / 2 : BN;  // output columns of a tile
     static_assert(!GU || (TN % 2 == 0 && !BKM), "gate and up tiles pair within a wave");
     // separate arrays, so that the compiler sees that the stream into one does not touch the other
-    __shared__ __attribute__((aligned(1024))) uint16_t as0[BM * kBK], as1[BM * kBK], as2[BM * kBK], as3[BM * kBK];
-    __shared__ __attribute__((aligned(1024))) uint16_t bs0[BN * kBK], bs1[BN * kBK], bs2[BN * kBK], bs3[BN * kBK];
+    __shared__ __attribute__((aligned(1024))) uint16_t as0[BM * BK], as1[BM * BK], as2[BM * BK], as3[BM * BK];
+    __shared__ __attribute__((aligned(1024))) uint16_t bs0[BN * BK], bs1[BN * BK], bs2[BN * BK], bs3[BN * BK];
     __shared__ f32x4 scratch[NW][256];
     const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wv / WN, wn = wv % WN;
 
-    Tile<BM, AK, NW> ta;
-    Tile<BN, BKM, NW, BNC> tb;
+    Tile<BM, BK, AK, NW> ta;
+    Tile<BN, BK, BKM, NW, BNC> tb;
     ta.init(wv, lane);
     tb.init(wv, lane);
 
     f32x16 acc[TM][TN];
     bf16x8 fa[2][TM], fb[2][TN];
 
-    const int ksteps = (g.K + kBK - 1) / kBK, nsteps = g.steps;  // filled up with steps of zeros
+    const int ksteps = (g.K + BK - 1) / BK, nsteps = g.steps;  // filled up with steps of zeros
     // The stream of loads: tile, step, segment and k of the next one, and what they read.  All of it is
     // kept in registers: a scalar load in the loop would wait for every LDS read in flight.
     int lv = blockIdx.x, lstep = 0, lseg = 0, lk = 0;
@@ -380,7 +383,7 @@ __global__ __launch_bounds__(64 * WM *WN, 1) void k_ffn_gemm(GemmArgs g)
         tb.turn(leftb, ldb);
         const int first = lp.part * nsteps;
         lseg = first / ksteps;
-        lk = (first - lseg * ksteps) * kBK;
+        lk = (first - lseg * ksteps) * BK;
         live = lseg < g.nseg;
         if (live) segment();
     };
@@ -396,15 +399,15 @@ __global__ __launch_bounds__(64 * WM *WN, 1) void k_ffn_gemm(GemmArgs g)
         if constexpr (GU) {
             const auto wu = tb.window(pu, leftb, ldb, lk, K, live);
 #pragma unroll
-            for (int i = 0; i < tb.kInstr; i++)  // sixteen rows, all of one matrix
-                tb.piece(((wv * tb.kInstr + i) >> 1) & 1 ? wu : w, bs, i, K - lk, wv);
+            for (int i = 0; i < tb.kInstr; i++)  // a load's rows are all of one matrix
+                tb.piece((tb.kRpi * (wv * tb.kInstr + i) >> 5) & 1 ? wu : w, bs, i, K - lk, wv);
         } else {
 #pragma unroll
             for (int i = 0; i < tb.kInstr; i++) tb.piece(w, bs, i, K - lk, wv);
         }
     };
     auto advance = [&] {
-        lk += kBK;
+        lk += BK;
         lstep++;
         if (lk < K && lstep < nsteps) return;
         if (lstep == nsteps) {
@@ -422,9 +425,9 @@ __global__ __launch_bounds__(64 * WM *WN, 1) void k_ffn_gemm(GemmArgs g)
     auto read = [&](auto P, const uint16_t *as, const uint16_t *bs, int s) {
         constexpr int p = decltype(P)::value;
 #pragma unroll
-        for (int j = 0; j < TN; j++) fb[p][j] = Tile<BN, BKM, NW, BNC>::frag(bs, 32 * (wn * TN + j), s, lane);
+        for (int j = 0; j < TN; j++) fb[p][j] = Tile<BN, BK, BKM, NW, BNC>::frag(bs, 32 * (wn * TN + j), s, lane);
 #pragma unroll
-        for (int i = 0; i < TM; i++) fa[p][i] = Tile<BM, AK, NW>::frag(as, 32 * (wm * TM + i), s, lane);
+        for (int i = 0; i < TM; i++) fa[p][i] = Tile<BM, BK, AK, NW>::frag(as, 32 * (wm * TM + i), s, lane);
     };
     // the B rows (output columns) take the MFMA's row side: a lane ends up with columns
     // 8 q + 4 (lane / 32) + 0..3 of row lane % 32
@@ -438,23 +441,36 @@ __global__ __launch_bounds__(64 * WM *WN, 1) void k_ffn_gemm(GemmArgs g)
     using E = std::integral_constant<int, 0>;
     using O = std::integral_constant<int, 1>;
     constexpr int kReads = TN * (BKM ? 2 : 1) + TM * (AK ? 2 : 1), kMul = TM * TN;
-    // One step of 32 k.  The fragments of the next 16 k are read while the present ones are multiplied, and
+    // One step of BK.  The fragments of the next 16 k are read while the present ones are multiplied, and
     // the loads of the step three further on are spread evenly over the matrix instructions (issued in a
     // bunch they fill the memory pipe's queue, and the wave that waits to issue the next one issues no
     // matrix instruction either).  One barrier a step, before its last 16 k: by then every wave has read
     // all of this buffer (the loads of the next step's turn may stream into it) and has seen its own part
-    // of the next step arrive (all but the newest loads: a step's, and half of another's).
+    // of the next step arrive (all but the newest loads: a step's, and what this step has issued).
+    constexpr int kSub = BK / 16;
+    auto meet = [&] {
+        wait_vm<ta.kInstr + tb.kInstr + (kSub > 2 ? ta.kInstr + tb.kInstr : ta.kInstr)>();
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    };
     auto step = [&](const uint16_t *as, const uint16_t *bs, const uint16_t *an, const uint16_t *bn, uint16_t *al, uint16_t *bl) {
         load_a(al);
         read(O(), as, bs, 1);
         mul(E());
         interleave<kReads, ta.kInstr, kMul>();
-        wait_vm<2 * ta.kInstr + tb.kInstr>();
-        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        load_b(bl);
+        if constexpr (kSub == 4) {
+            load_b(bl);
+            read(E(), as, bs, 2);
+            mul(O());
+            interleave<kReads, tb.kInstr, kMul>();
+            read(O(), as, bs, 3);
+            mul(E());
+            interleave<kReads, 0, kMul>();
+        }
+        meet();
+        if constexpr (kSub == 2) load_b(bl);
         read(E(), an, bn, 0);
         mul(O());
-        interleave<kReads, tb.kInstr, kMul>();
+        interleave<kReads, kSub == 2 ? tb.kInstr : 0, kMul>();
         advance();
     };
 
@@ -631,17 +647,17 @@ int64_t count_tiles(GemmArgs &g)
 }
 
 // slots: blocks that fit the card at once
-template <int BM, int BN, int WM, int WN, bool AK, bool BKM, int EPI, int ACT>
+template <int BM, int BN, int WM, int WN, int BK, bool AK, bool BKM, int EPI, int ACT>
 hipError_t go(GemmArgs g, int splits, int slots, hipStream_t s)
 {
-    const int64_t total = (int64_t)((g.K + kBK - 1) / kBK) * g.nseg;
+    const int64_t total = (int64_t)((g.K + BK - 1) / BK) * g.nseg;
     g.steps = (int)(((total + splits - 1) / splits + kBufs - 1) / kBufs * kBufs);
     g.splits = (int)((total + g.steps - 1) / g.steps);
     const int64_t tiles = count_tiles<BM, BN, EPI>(g) * g.splits;
     if (tiles > (int64_t)1 << 30) return hipErrorInvalidValue;
     g.tiles = (int)tiles;
     const unsigned grid = (unsigned)(tiles < slots ? tiles : slots);
-    hipLaunchKernelGGL((k_ffn_gemm<BM, BN, WM, WN, AK, BKM, EPI, ACT>), dim3(grid), dim3(64 * WM * WN), 0, s, g);
+    hipLaunchKernelGGL((k_ffn_gemm<BM, BN, WM, WN, BK, AK, BKM, EPI, ACT>), dim3(grid), dim3(64 * WM * WN), 0, s, g);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || g.splits == 1) return e;
     size_t most = 0;
@@ -652,36 +668,39 @@ hipError_t go(GemmArgs g, int splits, int slots, hipStream_t s)
 }
 
 // Microseconds that a product is expected to take with BM x BN tiles and its reduction cut in `splits`.
-// From timings of the five products at 1 to 8192 tokens, widths 512 to 14336 (the choice is within 10 % of
-// the best tile and split of each): a step of 32 k on one CU takes 0.72 us for a 256 x 256 tile, 0.27 for
-// 128 x 128 (two blocks share a CU, 0.55 for both; 0.24 alone, 0.36 waiting for memory) and 0.145 for 64 x 64
-// (four blocks; 0.21, 0.31 alone), so a
-// large tile does 1.5 and 3 times the work of the smaller ones in the same time, and wins where it fills
-// the card: 4096 tokens down 147 us against 223 and 381, but 1024 tokens d h 93 against 67 and 91.  What
-// comes back from a cut reduction crosses memory twice more in fp32 (6144 -> 3584 at 64 tokens: whole 41 us,
-// in eight parts 20).  Memory brings what the resident blocks have asked for, three steps each, in 1.2 us.
+// From timings of the products at 1 to 8192 tokens, widths 512 to 14336 (the choice takes 1 % more than the
+// best tile and cut in the mean, 15 % at most): a step on one CU takes 0.72 us for 256 x 256 tiles of 32 k,
+// and 0.47 and 0.23 for 128 x 128 and 64 x 64 tiles of 64 k, so that a large tile does 1.3 and 2.5 times the
+// work of the smaller ones in the same time, and wins where it fills the card: 4096 tokens down 147 us
+// against 223 and 381, but 1000 tokens d h 73 against 85 and 103, and 400 tokens d h 45 against 38 and 58.
+// What comes back from a cut reduction crosses memory twice more in fp32 (6144 -> 3584 at 64 tokens: whole
+// 34 us, in four parts 17).  Memory brings what the resident blocks have asked for, three steps each, in 1.2 us.
+// The small tiles take 64 k a step because rows of 128 bytes come from memory faster than rows of 64: with
+// 32 k, two and four blocks a CU and the same bytes on their way, d x of 400 tokens at 3584 x 6144 took 71 us
+// (54 with 64 k), its gate/up 68 (56), down 42 (33); nothing got slower by more than 3 %.
 struct Shape {
-    int rows, cols, resident;
+    int rows, cols, resident, bk;
     double step, cached, alone, tail;  // us per step beside others, per step alone (operands in the last-level cache, in memory), per tile's end
 };
-constexpr Shape kShapes[4] = {{256, 256, 1, 0.72, 0.54, 0.60, 6.0},
-                              {256, 192, 1, 0.64, 0.48, 0.53, 4.5},
-                              {128, 128, 2, 0.27, 0.24, 0.355, 1.5},
-                              {64, 64, 4, 0.145, 0.21, 0.31, 0.5}};
+constexpr Shape kShapes[4] = {{256, 256, 1, 32, 0.72, 0.54, 0.60, 6.0},
+                              {256, 192, 1, 32, 0.64, 0.48, 0.53, 4.5},
+                              {128, 128, 1, 64, 0.47, 0.47, 0.49, 0.6},
+                              {64, 64, 2, 64, 0.23, 0.28, 0.33, 0.0}};
 constexpr double kCached = 32e6;  // operands of fewer bytes are taken to be still cached from the call before
 
-double expected_us(const Shape &c, int64_t tiles, int64_t steps, int splits, int cus, int rows, double in_bytes, double out_bytes,
+double expected_us(const Shape &c, int64_t tiles, int64_t k, int splits, int cus, int rows, double in_bytes, double out_bytes,
                    double part_bytes)
 {
+    const int64_t steps = (k + c.bk - 1) / c.bk;
     const int64_t per = ((steps + splits - 1) / splits + kBufs - 1) / kBufs * kBufs, parts = (steps + per - 1) / per;
     const int64_t blocks = tiles * parts, n = (blocks + cus - 1) / cus;  // n: tiles of the busiest CU
     const double alone = in_bytes < kCached ? c.cached : c.alone, one = c.step * n > alone ? c.step * n : alone;
     double work = per * one + c.tail * n;
     const int64_t resident = blocks < (int64_t)c.resident * cus ? blocks : (int64_t)c.resident * cus;
-    const double asked = (double)resident * (kBufs - 1) * kBK * 2 * (c.cols + (rows < c.rows ? rows : c.rows));
-    const double rate = asked / 1.2 < 5e6 ? asked / 1.2 : 5e6, mem = in_bytes / rate;
+    const double asked = (double)resident * (kBufs - 1) * c.bk * 2 * (c.cols + (rows < c.rows ? rows : c.rows));
+    const double rate = asked / 1.2 < 5.4e6 ? asked / 1.2 : 5.4e6, mem = in_bytes / rate;
     if (mem > work) work = mem;
-    return 3.0 + work + out_bytes / 4.4e6 + (parts > 1 ? 2.0 + 2.0 * parts * part_bytes / 5e6 : 0.0);
+    return 3.5 + work + out_bytes / 4.4e6 + (parts > 1 ? 2.1 + 0.4 * parts + 2.0 * parts * part_bytes / 5.6e6 : 0.0);
 }
 
 struct Plan {
@@ -693,7 +712,7 @@ template <int EPI>
 Plan plan(GemmArgs &g, size_t part_floats)
 {
     const int cus = compute_units();
-    const int64_t steps = (int64_t)((g.K + kBK - 1) / kBK) * g.nseg;
+    const int64_t k = (int64_t)g.K * g.nseg;
     size_t floats = 0;
     double in = 0, out = 0;
     int rows = 0;
@@ -709,8 +728,8 @@ Plan plan(GemmArgs &g, size_t part_floats)
     const int64_t tiles[4] = {count_tiles<256, 256, EPI>(g), count_tiles<256, 192, EPI>(g), count_tiles<128, 128, EPI>(g), count_tiles<64, 64, EPI>(g)};
     Plan best;
     for (int c = 0; c < 4; c++)
-        for (int sp = 1; sp <= 16 && !(EPI == EPI_GU && c == 1) && (sp == 1 || (steps / sp >= kBufs && floats * sp <= part_floats)); sp++) {
-            const double t = expected_us(kShapes[c], tiles[c], steps, sp, cus, rows, in, out, 4.0 * floats);
+        for (int sp = 1; sp <= 16 && !(EPI == EPI_GU && c == 1) && (sp == 1 || (k / sp >= 128 && floats * sp <= part_floats)); sp++) {
+            const double t = expected_us(kShapes[c], tiles[c], k, sp, cus, rows, in, out, 4.0 * floats);
             if (t < best.us) best = {c, sp, t};
         }
     return best;
@@ -725,11 +744,11 @@ hipError_t gemm(GemmArgs g, float *part, size_t part_floats, hipStream_t s)
         g.p[i].part = part;
         part += (size_t)c.splits * g.p[i].M * g.p[i].N * (EPI == EPI_GU ? 2 : 1);
     }
-    if (c.shape == 0) return go<256, 256, 2, 2, AK, BKM, EPI, ACT>(g, c.splits, cus, s);
+    if (c.shape == 0) return go<256, 256, 2, 2, 32, AK, BKM, EPI, ACT>(g, c.splits, cus, s);
     if constexpr (EPI != EPI_GU)  // gate and up columns pair within a wave: an even number of tiles
-        if (c.shape == 1) return go<256, 192, 2, 2, AK, BKM, EPI, ACT>(g, c.splits, cus, s);
-    if (c.shape == 2) return go<128, 128, 2, 2, AK, BKM, EPI, ACT>(g, c.splits, 2 * cus, s);
-    return go<64, 64, 2, 1, AK, BKM, EPI, ACT>(g, c.splits, 4 * cus, s);
+        if (c.shape == 1) return go<256, 192, 2, 2, 32, AK, BKM, EPI, ACT>(g, c.splits, cus, s);
+    if (c.shape == 2) return go<128, 128, 2, 2, 64, AK, BKM, EPI, ACT>(g, c.splits, cus, s);
+    return go<64, 64, 2, 1, 64, AK, BKM, EPI, ACT>(g, c.splits, 2 * cus, s);
 }
 
 // Product i of g.
