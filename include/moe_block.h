@@ -34,7 +34,7 @@ extern "C" {
 /* y = act(x Wg^T, x Wu^T) Wd^T with bf16 weights Wg, Wu [I][D] and Wd [D][I], the activation a
  * moe_act of moe.h.  Products of bf16 values, fp32 accumulation; the activation is evaluated
  * in fp32.  What the second product reads follows the type asked for its result: for a bf16
- * result h = act(g, u) is rounded once to bf16 (2^-9 relative at most), for an fp32 result h
+ * result h = act(g, u) is rounded once to bf16 (2^-8 relative at most), for an fp32 result h
  * enters as three bf16 terms that hold its 24 bits.  The gradients' dg and du likewise. */
 typedef struct {
     int32_t width;       /* D: multiple of 8, at most 2^20 */
@@ -145,7 +145,8 @@ void moe_norm_destroy(moe_norm *h);
  *   v  = beta2 v + (1 - beta2) g'^2
  *   p  = p (1 - lr s wd) - lr s / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
  * with the tensor's own lr scale s and weight decay wd.  With max_norm > 0 a step whose gradient
- * norm is not finite changes nothing, the step count included.
+ * norm is not finite changes nothing, the step count included; squares are formed in fp32, so a gradient of
+ * 2^62 or more in size may count as not finite.
  *
  * MOE_STATE_E4M3 keeps m and sqrt(v) as OCP E4M3 codes, one byte each, with an fp32 scale for each
  * run of 256 consecutive elements of a tensor (the last run may be shorter): scale = max|.| / 448,
@@ -188,7 +189,9 @@ moe_status moe_adamw_create(const moe_adamw_desc *d, void *workspace, size_t ws_
 
 /* Take these tensors (the array is copied; the buffers are borrowed until the next bind or the destroy),
  * enqueueing their table's upload on the stream.  Nothing that a step writes may overlap another buffer
- * of the set (MOE_ERR_INVALID_ARG), so a tensor named twice is refused.  n = 0 tensors is allowed. */
+ * of the set (MOE_ERR_INVALID_ARG), so a tensor named twice is refused.  n = 0 tensors is allowed.
+ * A captured step works on the tensors that are bound when it is replayed: replay it only while they are as
+ * many and of the sizes it was captured with. */
 moe_status moe_adamw_bind(moe_adamw *a, const moe_adamw_tensor *t, int32_t n, void *stream);
 
 /* Set the number of steps taken so far (0 in a new run; kept on the device, so a captured step counts its

@@ -16,6 +16,12 @@
 // steps ahead of the multiplication.  The blocks are persistent: each walks tiles b, b + gridDim, ..., and the stream of
 // loads runs on into the next tile while the present one's results are stored through LDS scratch of
 // their own, so the matrix pipes wait neither for a first load nor for the last store.
+// At 8192 tokens, 7168 -> 14336 -> 7168: gate/up 2.87 ms (1.17 PFLOP/s; 1.28 without keeping g and u), down 1.60
+// (1.06), d h 1.70 (0.99), d x 2.72 (1.24), d W 3.78 (1.34); a library's product reaches 1.0 to 1.5 on the card.
+// Bound there by how fast 64-byte rows of the tiles arrive in LDS (43 to 58 GB/s a CU) and by the clock that
+// the card's power allows (1.8 to 2.0 GHz); d h and gate/up also by the fp32 g and u, whose bytes the epilogue
+// moves while no product runs on that CU.  64 k a step in two buffers, whose rows are 128 bytes, cannot ask
+// far enough ahead: d W 4.60 ms, d x 2.96.
 #include <type_traits>
 
 #include "block_internal.h"
@@ -763,7 +769,7 @@ Prob &prob(GemmArgs &g, int M, int N, int lda, int ldb, void *c)
 
 // What the few-token kernels of ffn_few.hip are expected to take: the weights at 5.6 TB/s, and the tokens,
 // which every block reads, from the caches.  At 3584 -> 6144 -> 3584 the two kernels take 18 and 11 us for one
-// token (the tiled products 29 and 19) and 46 and 35 for 64 (39 and 23).
+// token (the tiled products 22 and 15) and 46 and 35 for 64 (24 and 17).
 static double few_us(int T, int N, int K, int planes, bool pair)
 {
     const int tiles = T <= 16 ? 1 : T <= 32 ? 2 : 4, cols = pair ? (tiles == 1 ? 8 : 16) : 16;

@@ -7,7 +7,8 @@
 // turns of 64 k, a whole 128-byte line of each row; weights go straight from memory into MFMA operands
 // (lane l holds row l % 16, eight k from 8 (l / 16)), tokens likewise through the caches.  The waves'
 // sums meet in LDS and are added in wave order.
-// Bound by memory: at 3584 -> 6144 the gate and up rows are 88 MB, the down rows 44 MB.
+// Bound by memory: at 3584 -> 6144 the gate and up rows are 88 MB, the down rows 44 MB; one token takes 17.7
+// and 11.8 us (5.0 and 3.7 TB/s, a plain copy of such size 4.8).
 #include <type_traits>
 
 #include "block_internal.h"

