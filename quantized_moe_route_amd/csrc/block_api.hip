@@ -4,6 +4,7 @@
 #include <cmath>
 #include <initializer_list>
 #include <new>
+#include <utility>
 #include <vector>
 
 #include "api_status.h"
@@ -215,6 +216,15 @@ struct moe_adamw {
     bool bound = false, counted = false;
     int64_t chunks = 0;
     int chunk_elems = kChunk;
+    // the bytes that a step reads or writes, in address order and disjoint: the bound buffers and the workspace
+    std::vector<std::pair<uintptr_t, uintptr_t>> used;
+
+    bool uses(const void *p, size_t bytes) const
+    {
+        const uintptr_t lo = (uintptr_t)p, hi = lo + bytes;
+        const auto i = std::upper_bound(used.begin(), used.end(), lo, [](uintptr_t v, const auto &r) { return v < r.second; });
+        return p && i != used.end() && i->first < hi;
+    }
 };
 
 namespace {
@@ -560,12 +570,20 @@ try {
     }
     // in address order every range has to begin at or behind the end of what is written before it, and a
     // written one behind the end of everything before it
+    ranges.push_back({(uintptr_t)a->ws, (uintptr_t)a->ws + a->lay.total, true, -1});
     std::sort(ranges.begin(), ranges.end(), [](const Range &x, const Range &y) { return x.lo < y.lo; });
     uintptr_t end = 0, end_written = 0;
+    int last = -1;  // whose range ends at end
+    std::vector<std::pair<uintptr_t, uintptr_t>> used;
     for (const Range &r : ranges) {
         if (r.lo < (r.written ? end : end_written))
-            return api_fail(MOE_ERR_INVALID_ARG, "tensor %d: a buffer overlaps one that the step writes", r.tensor);
-        end = std::max(end, r.hi);
+            return api_fail(MOE_ERR_INVALID_ARG, "tensor %d: a buffer overlaps one that the step writes (a tensor's or the workspace)",
+                            r.tensor < 0 ? last : r.tensor);
+        if (used.empty() || r.lo > end)
+            used.push_back({r.lo, r.hi});
+        else
+            used.back().second = std::max(end, r.hi);
+        if (r.hi > end) end = r.hi, last = r.tensor;
         if (r.written) end_written = std::max(end_written, r.hi);
     }
     const int ce = chunk_for(total);
@@ -583,6 +601,7 @@ try {
     a->bound = true;
     a->chunks = chunks;
     a->chunk_elems = ce;
+    a->used.swap(used);
     return MOE_OK;
 } catch (...) {
     return MOE_ERR_INTERNAL;  // out of host memory: no text, which would need some
@@ -608,6 +627,9 @@ moe_status moe_adamw_step(moe_adamw *a, double lr, const float *lr_dev, float *g
     if (!lr_dev && !std::isfinite(lr)) return api_fail(MOE_ERR_INVALID_ARG, "lr=%g is not finite", lr);
     if (!on(lr_dev, 4) || !on(grad_norm, 4)) return api_fail(MOE_ERR_INVALID_ARG, "lr_dev or grad_norm is not aligned to its element");
     if (grad_norm && !(a->d.max_norm > 0)) return api_fail(MOE_ERR_INVALID_ARG, "grad_norm needs max_norm > 0");
+    if (a->uses(grad_norm, 4)) return api_fail(MOE_ERR_INVALID_ARG, "grad_norm overlaps a bound tensor or the workspace");
+    if (lr_dev && grad_norm && (uintptr_t)lr_dev < (uintptr_t)grad_norm + 4 && (uintptr_t)grad_norm < (uintptr_t)lr_dev + 4)
+        return api_fail(MOE_ERR_INVALID_ARG, "grad_norm overlaps lr_dev");
     moe::AdamArgs s{};
     s.tab = (const moe::AdamTensor *)(a->ws + a->lay.tab);
     s.chunk_of = (const uint32_t *)(a->ws + a->lay.map);

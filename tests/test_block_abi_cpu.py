@@ -156,6 +156,8 @@ def test_adamw_refusals():
         assert bind(tensor(**kw)) == BAD, kw
     assert bind(ok, ok) == BAD and b"overlaps" in L.moe_last_error()
     assert bind(ok, tensor(1, m=ok.m)) == BAD and bind(ok, tensor(1, param=ok.grad)) == BAD
+    for kw in (dict(grad=WS), dict(m=WS + size("adamw", d)[1] - 4)):
+        assert bind(tensor(**kw)) == BAD and b"workspace" in L.moe_last_error(), kw
     assert bind(ok, tensor(1), tensor(2)) == BAD  # more than max_tensors
     assert bind(tensor(n=1001), tensor(1)) == BAD  # more than max_elements
     assert L.moe_adamw_bind(h, None, 1, None) == BAD and L.moe_adamw_bind(None, None, 0, None) == BAD

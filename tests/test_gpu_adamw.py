@@ -260,3 +260,10 @@ def test_python_refusals():
         o.step(1e-3, grad_norm=torch.zeros(1, device="cuda"))  # without max_norm
     with pytest.raises(q.MoeError):
         o.set_step(-1)
+    before = [t.clone() for t in p]
+    o = q.AdamW(p, g, **st, max_norm=1.0)
+    lr = torch.full((1,), 1e-3, device="cuda")
+    for taken in (p[0].view(-1)[:1], g[1].view(-1)[-1:], o.m[0].view(-1)[1:2], lr):  # the norm where the step reads or writes
+        with pytest.raises(q.MoeError):
+            o.step(lr, grad_norm=taken)
+    assert all(torch.equal(a, b) for a, b in zip(before, p))
