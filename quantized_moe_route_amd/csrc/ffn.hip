@@ -58,6 +58,7 @@ struct GemmArgs {
     int tiles;            // of all products, times splits (set by the launcher, as the next two)
     int splits;           // parts of the reduction, each a tile of its own in the list
     int steps;            // steps of a part, a multiple of kBufs
+    int fold;             // > 1: M is this many times the rows of the result, each M / fold rows a term of A; k_ffn_join adds the terms
     const uint16_t *b2;   // EPI_GU: the up matrix (b of the segment is the gate matrix)
     int ct;               // EPI_STORE: dtype of c
     bool acc;
@@ -525,7 +526,7 @@ __global__ __launch_bounds__(64 * WM *WN, 1) void k_ffn_gemm(GemmArgs g)
                 if (mb + r < M && nb + 8 * lc < N) f(h, mb + r, nb + 8 * lc, x);
             }
         };
-        if (g.splits > 1) {
+        if (g.splits > 1 || g.fold > 1) {
             // the part's sums as they are, for k_ffn_join
             const int W = GU ? 2 * N : N;
             float *const part = g.p[at.p].part + (size_t)at.part * M * W;
@@ -606,7 +607,7 @@ __global__ __launch_bounds__(256) void k_ffn_join(GemmArgs g)
 {
     constexpr bool GU = EPI == EPI_GU;
     const Prob &p = g.p[blockIdx.y];
-    const int M = p.M, N = p.N, W = GU ? 2 * N : N, per = N / 8;
+    const int fold = max(g.fold, 1), M = p.M / fold, N = p.N, terms = g.splits * fold, W = GU ? 2 * N : N, per = N / 8;
     const size_t stride = (size_t)M * W, total = (size_t)M * per;
     for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (size_t)gridDim.x * 256) {
         const int m = (int)(i / per), n = 8 * (int)(i % per);
@@ -614,7 +615,7 @@ __global__ __launch_bounds__(256) void k_ffn_join(GemmArgs g)
         float v[8], u[8];
 #pragma unroll
         for (int e = 0; e < 8; e++) v[e] = u[e] = 0.f;
-        for (int s = 0; s < g.splits; s++) {
+        for (int s = 0; s < terms; s++) {
             const float *q = src + s * stride;
             const f32x4 a = *(const f32x4 *)q, b = *(const f32x4 *)(q + 4);
 #pragma unroll
@@ -665,9 +666,10 @@ hipError_t go(GemmArgs g, int splits, int slots, hipStream_t s)
     const unsigned grid = (unsigned)(tiles < slots ? tiles : slots);
     hipLaunchKernelGGL((k_ffn_gemm<BM, BN, WM, WN, BK, AK, BKM, EPI, ACT>), dim3(grid), dim3(64 * WM * WN), 0, s, g);
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || g.splits == 1) return e;
+    if (e != hipSuccess || (g.splits == 1 && g.fold <= 1)) return e;
     size_t most = 0;
     for (int i = 0; i < g.np; i++) most = most > (size_t)g.p[i].M * g.p[i].N ? most : (size_t)g.p[i].M * g.p[i].N;
+    if (g.fold > 1) most /= g.fold;
     const size_t blocks = (most / 8 + 255) / 256;
     hipLaunchKernelGGL((k_ffn_join<EPI, ACT>), dim3((unsigned)(blocks < 2048 ? blocks : 2048), (unsigned)g.np), dim3(256), 0, s, g);
     return hipGetLastError();
@@ -694,7 +696,7 @@ constexpr Shape kShapes[4] = {{256, 256, 1, 32, 0.72, 0.54, 0.60, 6.0},
                               {64, 64, 2, 64, 0.23, 0.28, 0.33, 0.0}};
 constexpr double kCached = 32e6;  // operands of fewer bytes are taken to be still cached from the call before
 
-double expected_us(const Shape &c, int64_t tiles, int64_t k, int splits, int cus, int rows, double in_bytes, double out_bytes,
+double expected_us(const Shape &c, int64_t tiles, int64_t k, int splits, int fold, int cus, int rows, double in_bytes, double out_bytes,
                    double part_bytes)
 {
     const int64_t steps = (k + c.bk - 1) / c.bk;
@@ -706,7 +708,7 @@ double expected_us(const Shape &c, int64_t tiles, int64_t k, int splits, int cus
     const double asked = (double)resident * (kBufs - 1) * c.bk * 2 * (c.cols + (rows < c.rows ? rows : c.rows));
     const double rate = asked / 1.2 < 5.4e6 ? asked / 1.2 : 5.4e6, mem = in_bytes / rate;
     if (mem > work) work = mem;
-    return 3.5 + work + out_bytes / 4.4e6 + (parts > 1 ? 2.1 + 0.4 * parts + 2.0 * parts * part_bytes / 5.6e6 : 0.0);
+    return 3.5 + work + out_bytes / 4.4e6 + (parts > 1 || fold > 1 ? 2.1 + 0.4 * parts * fold + 2.0 * parts * part_bytes / 5.6e6 : 0.0);
 }
 
 struct Plan {
@@ -717,7 +719,7 @@ struct Plan {
 template <int EPI>
 Plan plan(GemmArgs &g, size_t part_floats)
 {
-    const int cus = compute_units();
+    const int cus = compute_units(), fold = g.fold > 1 ? g.fold : 1;
     const int64_t k = (int64_t)g.K * g.nseg;
     size_t floats = 0;
     double in = 0, out = 0;
@@ -727,15 +729,15 @@ Plan plan(GemmArgs &g, size_t part_floats)
         const double mn = (double)p.M * p.N, wide = EPI == EPI_GU ? 2 : 1;
         floats += (size_t)p.M * p.N * (EPI == EPI_GU ? 2 : 1);
         in += 2.0 * g.K * g.nseg * (p.M + wide * p.N);
-        out += EPI == EPI_STORE ? mn * (g.ct == DT_F32 ? 4 : 2)
+        out += EPI == EPI_STORE ? mn / fold * (g.ct == DT_F32 ? 4 : 2)
                                 : EPI == EPI_GU ? mn * (2 * (g.h ? g.planes : 0) + (g.gu ? 8 : 0)) : mn * (8 + 2 * g.planes * ((g.h ? 1 : 0) + (g.dgu ? 2 : 0)));
         rows = rows > p.M ? rows : p.M;
     }
     const int64_t tiles[4] = {count_tiles<256, 256, EPI>(g), count_tiles<256, 192, EPI>(g), count_tiles<128, 128, EPI>(g), count_tiles<64, 64, EPI>(g)};
     Plan best;
     for (int c = 0; c < 4; c++)
-        for (int sp = 1; sp <= 16 && !(EPI == EPI_GU && c == 1) && (sp == 1 || (k / sp >= 128 && floats * sp <= part_floats)); sp++) {
-            const double t = expected_us(kShapes[c], tiles[c], k, sp, cus, rows, in, out, 4.0 * floats);
+        for (int sp = 1; sp <= 16 && !(EPI == EPI_GU && c == 1) && ((sp == 1 && fold == 1) || ((sp == 1 || k / sp >= 128) && floats * sp <= part_floats)); sp++) {
+            const double t = expected_us(kShapes[c], tiles[c], k, sp, fold, cus, rows, in, out, 4.0 * floats);
             if (t < best.us) best = {c, sp, t};
         }
     return best;
@@ -755,6 +757,20 @@ hipError_t gemm(GemmArgs g, float *part, size_t part_floats, hipStream_t s)
         if (c.shape == 1) return go<256, 192, 2, 2, 32, AK, BKM, EPI, ACT>(g, c.splits, cus, s);
     if (c.shape == 2) return go<128, 128, 2, 2, 64, AK, BKM, EPI, ACT>(g, c.splits, cus, s);
     return go<64, 64, 2, 1, 64, AK, BKM, EPI, ACT>(g, c.splits, 2 * cus, s);
+}
+
+// The rows of g's one product are terms whose sum is A: g.nseg / terms segments for each of them.  Taken as
+// segments, every term reads B again; taken as rows of their own (`fold`), B is read once and the terms'
+// sums are joined like parts.  With few tokens B is all there is to read, and the terms' rows fill a tile
+// that one term leaves empty: d x of 4 tokens at 6632 x 8008 in fp32 132 -> 60 us, the whole training pass
+// of 16 at 3584 x 6144 180 -> 156; with many the rows are tiles of their own, as the segments were, and the
+// join is on top.
+GemmArgs best_fold(GemmArgs g, int terms, size_t part_floats)
+{
+    GemmArgs f = g;
+    f.fold = terms, f.nseg = g.nseg / terms, f.p[0].M *= terms;
+    if (terms > 1 && (int64_t)g.p[0].M * terms < (int64_t)1 << 24 && plan<EPI_STORE>(f, part_floats).us < plan<EPI_STORE>(g, part_floats).us) return f;
+    return g;
 }
 
 // Product i of g.
@@ -799,6 +815,7 @@ hipError_t launch_ffn_forward(const FfnArgs &a, hipStream_t s)
     Prob &p = prob(g, a.T, a.D, a.I, a.I, a.y);
     g.nseg = planes, g.K = a.I, g.ct = a.yt, g.acc = a.acc;
     for (int k = 0; k < planes; k++) p.a[k] = a.h + (size_t)k * a.T * a.I, p.b[k] = a.wd;
+    g = best_fold(g, planes, a.part_floats);
     if (a.T <= kFewTokens && few_us(a.T, a.D, a.I, planes, false) < plan<EPI_STORE>(g, a.part_floats).us) return launch_ffn_few_down(a, planes, s);
     return gemm<false, false, EPI_STORE>(g, a.part, a.part_floats, s);
 }
@@ -834,6 +851,7 @@ hipError_t launch_ffn_backward(const FfnArgs &a, hipStream_t s)
             p.a[2 * k] = a.dgu + k * T * 2 * I, p.b[2 * k] = a.wg;
             p.a[2 * k + 1] = a.dgu + k * T * 2 * I + I, p.b[2 * k + 1] = a.wu;
         }
+        g = best_fold(g, px, a.part_floats);
         if ((e = gemm<false, true, EPI_STORE>(g, a.part, a.part_floats, s)) != hipSuccess) return e;
     }
     if (pw) {

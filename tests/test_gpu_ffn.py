@@ -75,6 +75,26 @@ def test_every_tile_shape(T, D, I):
             close(a, b, dt, K, n)
 
 
+# few tokens and much weight in fp32: the three terms of an operand are rows of their own, joined afterwards
+@pytest.mark.parametrize("T,D,I", [(1, 4104, 2056), (4, 3336, 4008), (21, 2048, 3000), (22, 2048, 3000), (43, 1536, 5000), (64, 3000, 1504)])
+def test_terms_as_rows(T, D, I):
+    c = make(T, D, I)
+    f = layer(c, T)
+    K = 2 * max(D, I)
+    (dx, *dw), _ = ref.ffn_grads("swiglu", *(c[k] for k in ("x", "wg", "wu", "wd", "dy")))
+    want = ref.ffn("swiglu", c["x"], c["wg"], c["wu"], c["wd"])
+    base = torch.randn(T, D, device="cuda")
+    y = base.clone()
+    close(f.forward(c["x"], out_dtype=F32), want, F32, K, "y")
+    close(f.forward(c["x"], y, accumulate=True), want + base.to(F64), F32, K, "y added")
+    got = f.backward(c["x"], c["dy"], dx_dtype=F32, dw_dtype=F32)
+    for a, b, n in zip((got[0], *got[1]), (dx, *dw), ("dx", "dw_gate", "dw_up", "dw_down")):
+        close(a, b, F32, K, n)
+    g = torch.full((T + 1, D), 5.0, device="cuda")
+    f.backward(c["x"], c["dy"], dx=g[:T], need_dw=False)
+    assert torch.equal(g[:T], got[0]) and (g[T] == 5).all()
+
+
 @pytest.mark.parametrize("T,D,I", [(1, 256, 128), (5, 264, 136), (100, 328, 264)])
 @pytest.mark.parametrize("dt", [BF16, F32])
 def test_accumulate_adds_onto_what_is_there(T, D, I, dt):
